@@ -81,7 +81,7 @@ typedef enum wqbmm_status {
   WQBMM_OK = 0,
   WQBMM_ERR_NULLPTR = 1,     /* a required pointer is NULL                       */
   WQBMM_ERR_INVALID = 2,     /* a shape / alignment rule above is violated       */
-  WQBMM_ERR_UNSUPPORTED = 3, /* group_size not 64/128, or the device is not gfx950 */
+  WQBMM_ERR_UNSUPPORTED = 3, /* group_size not 64/128, an unknown type (wqbmm_mxfp4.h), or the device is not gfx950 */
   WQBMM_ERR_LAUNCH = 4,      /* a HIP call or kernel launch failed               */
   WQBMM_ERR_ALLOC = 5,       /* workspace allocation failed                      */
   WQBMM_ERR_CAPTURE = 6,     /* the workspace would have to grow during graph capture */

@@ -13,7 +13,16 @@ y: fp16 [M][N].  The optional operand form of the weights (FP6 MFMA operand
 tiles, 0.75 byte per weight) spares the group-size-128 prefill path its
 per-call weight conversion; results are bit-identical with or without it.
 
-The method is the multi-step decomposition (MSD) of the page
+Beside it stand the microscaled 4-bit (MXFP4) operators of
+include/wqbmm_mxfp4.h (see _mxfp4.py):
+
+    codes, scales = wqbmm_mxfp4_quantize(x)           # any 16-bit or fp32 matrix
+    x2 = wqbmm_mxfp4_dequantize(codes, scales, x.dtype)
+    w = wqbmm_mxfp4_tile_weights(codes, scales)       # once per weight [N][K]
+    y = wqbmm_mxfp4_matmul(x, w, N)                   # or activations="mxfp4"
+    y, ids, weights = wqbmm_mxfp4_moe(x, router, gate_up, down, I, top_k)
+
+The method of the int4 operator is the multi-step decomposition (MSD) of the page
 "WeightQuantBatchMatmulExperiment 算子深度解析：A16W4 PerGroup 伪量化 MatMul 的
 MSD 算法与双模板流水设计" (lpnh.cn/news/2294145), §4.1.  Everything runs in
 the HIP kernels of libwqbmm.so behind the C ABI of include/wqbmm.h; these
@@ -22,6 +31,8 @@ current HIP stream.  PyTorch supplies device memory and streams.
 """
 from __future__ import annotations
 
+from ._mxfp4 import (wqbmm_mxfp4_dequantize, wqbmm_mxfp4_matmul, wqbmm_mxfp4_moe,  # noqa: F401
+                     wqbmm_mxfp4_quantize, wqbmm_mxfp4_tile_weights)
 from ._lib import (WQBMM_ERR_ALLOC, WQBMM_ERR_CAPTURE, WQBMM_ERR_INVALID,  # noqa: F401
                    WQBMM_ERR_LAUNCH, WQBMM_ERR_NULLPTR, WQBMM_ERR_TOO_LARGE,
                    WQBMM_ERR_UNSUPPORTED, WQBMM_OK, WQBMM_PATH_AUTO,
@@ -33,6 +44,8 @@ __all__ = [
     "wqbmm_a16w4_msd_path", "wqbmm_a16w4_msd_noalloc",
     "wqbmm_a16w4_msd_prepass",
     "wqbmm_a16w4_msd_yint", "wqbmm_a16w4_msd_profile_stage", "wqbmm_select_path", "wqbmm_status_string", "wqbmm_version",
+    "wqbmm_mxfp4_quantize", "wqbmm_mxfp4_dequantize", "wqbmm_mxfp4_tile_weights",
+    "wqbmm_mxfp4_matmul", "wqbmm_mxfp4_moe",
     "WqbmmError",
 ]
 

@@ -26,6 +26,13 @@ WQBMM_ERR_ALLOC = 5
 WQBMM_ERR_CAPTURE = 6
 WQBMM_ERR_TOO_LARGE = 7
 
+WQBMM_DTYPE_F16 = 0
+WQBMM_DTYPE_BF16 = 1
+WQBMM_DTYPE_F32 = 2
+
+WQBMM_MXFP4_ACT_16BIT = 0
+WQBMM_MXFP4_ACT_MXFP4 = 1
+
 WQBMM_PATH_AUTO = 0
 WQBMM_PATH_DECODE = 1
 WQBMM_PATH_PREFILL = 2
@@ -50,6 +57,13 @@ SIGNATURES = {
     "wqbmm_select_path": (_int, [_i64, _i64, _i64, _i64]),
     "wqbmm_status_string": (ctypes.c_char_p, [_int]),
     "wqbmm_version": (_int, []),
+    # include/wqbmm_mxfp4.h
+    "wqbmm_mxfp4_quantize": (_int, [_p, _int, _i64, _i64, _i64, _p, _p, _p]),
+    "wqbmm_mxfp4_dequantize": (_int, [_p, _p, _i64, _i64, _p, _int, _i64, _p]),
+    "wqbmm_mxfp4_tiled_weight_bytes": (_i64, [_i64, _i64]),
+    "wqbmm_mxfp4_tile_weights": (_int, [_p, _p, _i64, _i64, _p, _p]),
+    "wqbmm_mxfp4_matmul": (_int, [_p, _int, _i64, _p, _i64, _i64, _i64, _p, _int, _p]),
+    "wqbmm_mxfp4_moe": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p, _p]),
     # include/wqbmm_probe.h (measurement helper)
     "wqbmm_probe_stream_read": (_int, [_p, _i64, _p, _p]),
     "wqbmm_probe_mfma_valu": (_int, [_int, _int, _p, _p]),

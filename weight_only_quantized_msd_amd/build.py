@@ -16,7 +16,9 @@ CSRC = os.path.join(_HERE, "csrc")
 BUILD_DIR = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_HERE, "libwqbmm.so")
 SOURCES = ["msd_api.cpp", "msd_prepack.hip", "msd_prepass.hip", "msd_prefill.hip", "msd_prefill64.hip",
-           "msd_decode.hip", "msd_decode_gemv.hip", "msd_probe.hip"]
+           "msd_decode.hip", "msd_decode_gemv.hip", "msd_probe.hip",
+           "mx_api.cpp", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "mx_moe.hip"]
+HOST_SOURCES = ["msd_api.cpp", "mx_api.cpp"]   # argument validation, dispatch, workspace
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CFLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -53,28 +55,30 @@ def build(verbose: bool = False) -> str:
 
 
 def build_host_sanitized(verbose: bool = False) -> str:
-    """libwqbmm_san.so: the library with its host code (msd_api.cpp: argument
+    """libwqbmm_san.so: the library with its host code (HOST_SOURCES: argument
     validation, dispatch, workspace bookkeeping) built with AddressSanitizer
     and UndefinedBehaviorSanitizer; device code and the kernel objects are the
     normal ones (build() must have run).  The process that loads it must
     preload clang's ASan runtime.  The sanitizers apply to host code only."""
-    objs = [os.path.join(BUILD_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES if s != "msd_api.cpp"]
+    objs = [os.path.join(BUILD_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES if s not in HOST_SOURCES]
     for o in objs:
         if not os.path.exists(o):
             raise RuntimeError(f"{o} missing: run build() first")
-    api_obj = os.path.join(BUILD_DIR, "msd_api_san.o")
-    cmd = [HIPCC, "-x", "hip"] + CFLAGS + ["-g", "-Xarch_host", "-fsanitize=address",
-                                             "-Xarch_host", "-fsanitize=undefined",
-                                             "-Xarch_host", "-fno-sanitize-recover=all",
-                                             "-c", os.path.join(CSRC, "msd_api.cpp"), "-o", api_obj]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed on msd_api.cpp (sanitized):\n{r.stdout}\n{r.stderr}")
+    api_objs = []
+    for src in HOST_SOURCES:
+        api_objs.append(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + "_san.o"))
+        cmd = [HIPCC, "-x", "hip"] + CFLAGS + ["-g", "-Xarch_host", "-fsanitize=address",
+                                                 "-Xarch_host", "-fsanitize=undefined",
+                                                 "-Xarch_host", "-fno-sanitize-recover=all",
+                                                 "-c", os.path.join(CSRC, src), "-o", api_objs[-1]]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed on {src} (sanitized):\n{r.stdout}\n{r.stderr}")
     out = os.path.join(_HERE, "libwqbmm_san.so")
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Xarch_host", "-fsanitize=address",
-           "-Xarch_host", "-fsanitize=undefined", "-shared-libsan", "-o", out + ".tmp", api_obj] + objs
+           "-Xarch_host", "-fsanitize=undefined", "-shared-libsan", "-o", out + ".tmp"] + api_objs + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

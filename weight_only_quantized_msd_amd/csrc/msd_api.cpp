@@ -22,6 +22,7 @@
 
 #include "../../include/wqbmm.h"
 #include "msd_launch.hpp"
+#include "mx_launch.hpp"
 
 namespace {
 
@@ -192,6 +193,31 @@ wqbmm_status get_workspace(int dev, hipStream_t stream, const Needs& need, Buffe
 
 }  // namespace
 
+// ---- the same services for the other operators of the library (mx_launch.hpp)
+namespace wqbmm {
+
+wqbmm_status host_check_device(int* dev_out) noexcept { return check_device(dev_out); }
+
+wqbmm_status host_workspace(int dev, hipStream_t stream, size_t bytes, uint8_t** ws) noexcept {
+  *ws = nullptr;
+  if (bytes == 0) return WQBMM_OK;
+  try {
+    Needs need;
+    need.ops = round_up(bytes, 256);
+    Buffers b;
+    const wqbmm_status st = get_workspace(dev, stream, need, &b);
+    if (st != WQBMM_OK) return st;
+    *ws = b.ops;
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_ws[std::make_pair(dev, stream)].prep_path = 0;   // the call overwrites prepared operands
+  } catch (...) {
+    return WQBMM_ERR_ALLOC;
+  }
+  return WQBMM_OK;
+}
+
+}  // namespace wqbmm
+
 // ---- scratch of the allocation-free entry point (wqbmm_a16w4_msd_noalloc)
 // One fixed array per device, loaded with the library: the first 2 MiB hold
 // the fused decode kernel's split-K accumulators (zeroed at set-up, left zero
@@ -360,7 +386,7 @@ const char* wqbmm_status_string(int status) {
     case WQBMM_OK: return "WQBMM_OK";
     case WQBMM_ERR_NULLPTR: return "WQBMM_ERR_NULLPTR: a required pointer is NULL";
     case WQBMM_ERR_INVALID: return "WQBMM_ERR_INVALID: shape, range or alignment rule violated";
-    case WQBMM_ERR_UNSUPPORTED: return "WQBMM_ERR_UNSUPPORTED: group_size not 64/128 or device not gfx950";
+    case WQBMM_ERR_UNSUPPORTED: return "WQBMM_ERR_UNSUPPORTED: group_size not 64/128, an unknown type, or device not gfx950";
     case WQBMM_ERR_LAUNCH: return "WQBMM_ERR_LAUNCH: a HIP call or kernel launch failed";
     case WQBMM_ERR_ALLOC: return "WQBMM_ERR_ALLOC: workspace allocation failed";
     case WQBMM_ERR_TOO_LARGE:
