@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm16_kernel(const uint16_
   const int m0 = at.rb * BM, p0 = at.cb * (BN / 16);
   const int kt_lo = at.split * kq_per * 4, kt_hi = min(w.kt, kt_lo + kq_per * 4);
 
-  auto stage = [&](int kt, uint8_t* sx, uint8_t* sw) {
+  auto stage = [&](int kt, uint8_t* sx, uint8_t* sw) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < XP / WAVES; ++c) {
       const int pc = wave * (XP / WAVES) + c;
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm16_kernel(const uint16_
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[c][t] = mx_f4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](auto split_c, int kt, const uint8_t* sx, const uint8_t* sw) {
+  auto compute = [&](auto split_c, int kt, const uint8_t* sx, const uint8_t* sw) __attribute__((always_inline)) {
     constexpr bool SPLIT = decltype(split_c)::value;
     uint4 codes[TN];
     float f[TN];
@@ -177,10 +177,10 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm16_kernel(const uint16_
   // Two named buffers in turn: the next K-tile is copied into one while the
   // other is multiplied; each wave waits for its own copies, and the barrier
   // publishes all of them and frees the buffer just read.
-  auto run = [&](auto split_c) {
+  auto run = [&](auto split_c) __attribute__((always_inline)) {
     load_scales(kt_lo / 4, sc);
     load_scales(kt_lo / 4 + 1, sc_next);
-    auto advance = [&](int kt) {            // after K-tile kt: the next quad's scales
+    auto advance = [&](int kt) __attribute__((always_inline)) {            // after K-tile kt: the next quad's scales
       if ((kt & 3) == 3) {
 #pragma unroll
         for (int c = 0; c < TN; ++c) sc[c] = sc_next[c];
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm4_kernel(MxTiled x, MxT
   const int x0 = at.rb * (BM / 16), p0 = at.cb * (BN / 16);
   const int q_lo = at.split * kq_per, q_hi = min(w.kq, q_lo + kq_per);
 
-  auto copy = [&](const MxTiled& a, int first, int pieces, int kt, uint8_t* s) {
+  auto copy = [&](const MxTiled& a, int first, int pieces, int kt, uint8_t* s) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < pieces / WAVES; ++c) {
       const int pc = wave * (pieces / WAVES) + c;
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm4_kernel(MxTiled x, MxT
       __builtin_amdgcn_global_load_lds(a.codes + ((p * a.kt + k) * 64 + lane) * 16, s + pc * 1024, 16, 0, 0);
     }
   };
-  auto stage = [&](int kt, uint8_t* sx, uint8_t* sw) {
+  auto stage = [&](int kt, uint8_t* sx, uint8_t* sw) __attribute__((always_inline)) {
     copy(x, x0, XP, kt, sx);
     copy(w, p0, WP, kt, sw);
   };
@@ -320,9 +320,9 @@ __global__ __launch_bounds__(64 * WVM * WVN) void mx_gemm4_kernel(MxTiled x, MxT
   uint32_t scx[TM], scw[TN], nx[TM], nw[TN];
 
   // The K-tiles 4q + 2h, 4q + 2h + 1 from one buffer; h picks the scale bytes.
-  auto compute = [&](auto hc, int q, const uint8_t* sx, const uint8_t* sw) {
+  auto compute = [&](auto hc, int q, const uint8_t* sx, const uint8_t* sw) __attribute__((always_inline)) {
     constexpr int h = decltype(hc)::value;
-    auto tile = [&](auto ic) {
+    auto tile = [&](auto ic) __attribute__((always_inline)) {
       constexpr int i = decltype(ic)::value;
       if (4 * q + 2 * h + i >= w.kt) return;
       uint4 a[TN], b[TM];
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict_
   }
 }
 
-constexpr int GEMM_BM = 128, GEMM_BN = 128;
+constexpr int GEMM_BM = 128, GEMM_BN = 256;
 
 MxGemmPlan mx_gemm_plan(int64_t M, int64_t K, int64_t N, int act) {
   MxGemmPlan p{};
@@ -426,10 +426,10 @@ static hipError_t gemm_dt(const void* x, int64_t ldx, const MxTiled& w, int64_t 
     e = mx_launch(mx_prep_kernel<DT>, dim3((unsigned)((waves + 3) / 4)), dim3(256), stream, xp, ldx, m, blocks, xt.kt,
                   xt.kq, waves, codes, scales);
     if (e != hipSuccess) return e;
-    e = mx_launch(mx_gemm4_kernel<DT, GEMM_BM, GEMM_BN, 2, 2>, grid, dim3(256), stream, xt, w, m, N, mb, nb, sp, kp,
+    e = mx_launch(mx_gemm4_kernel<DT, GEMM_BM, GEMM_BN, 2, 4>, grid, dim3(512), stream, xt, w, m, N, mb, nb, sp, kp,
                   yp, part);
   } else {
-    e = mx_launch(mx_gemm16_kernel<DT, GEMM_BM, GEMM_BN, 2, 2>, grid, dim3(256), stream, xp, ldx, w, m, blocks, N, mb,
+    e = mx_launch(mx_gemm16_kernel<DT, GEMM_BM, GEMM_BN, 2, 4>, grid, dim3(512), stream, xp, ldx, w, m, blocks, N, mb,
                   nb, sp, kp, yp, part);
   }
   if (e != hipSuccess || sp == 1) return e;
