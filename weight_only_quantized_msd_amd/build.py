@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_HERE, "libwqbmm.so")
 SOURCES = ["msd_api.cpp", "msd_prepack.hip", "msd_prepass.hip", "msd_prefill.hip", "msd_prefill64.hip",
            "msd_decode.hip", "msd_decode_gemv.hip", "msd_probe.hip",
-           "mx_api.cpp", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "mx_moe.hip"]
+           "mx_api.cpp", "mx_quant.hip", "mx_gemv.hip", "mx_gemm16.hip", "mx_gemm4.hip", "mx_moe.hip"]
 HOST_SOURCES = ["msd_api.cpp", "mx_api.cpp"]   # argument validation, dispatch, workspace
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CFLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
@@ -28,9 +28,20 @@ CFLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=
           "-Wall", "-Wno-unused-function"]
 
 
+# the tiled MXFP4 products keep their results in AGPRs, by hand
+AGPR_SOURCES = ["mx_gemm16.hip", "mx_gemm4.hip"]
+
+
+def _flags(src: str) -> list:
+    if src not in AGPR_SOURCES:
+        return CFLAGS
+    at = CFLAGS.index("-amdgpu-mfma-vgpr-form=1")
+    return CFLAGS[:at - 1] + CFLAGS[at + 1:]
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC] + _flags(src) + ["-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd = [HIPCC, "-x", "hip"] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:

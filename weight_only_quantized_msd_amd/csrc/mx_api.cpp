@@ -85,11 +85,21 @@ wqbmm_status wqbmm_mxfp4_matmul(const void* x, int dtype, int64_t ldx, const voi
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const MxTiled w = mx_view(w_tiled, K, N);
   if (M <= kMxGemvMaxM) return status_of(launch_mx_gemv(x, dtype, ldx, w, M, K, N, y, act, s));
-  const MxGemmPlan plan = mx_gemm_plan(M, K, N, act);
+  if (!act && ldx >= kMxGemmMaxLd) {     // the tiled product addresses a tile of x with 31 bits
+    for (int64_t m = 0; m < M; m += kMxGemvMaxM) {
+      const hipError_t e = launch_mx_gemv(static_cast<const char*>(x) + m * ldx * 2, dtype, ldx, w,
+                                          M - m < kMxGemvMaxM ? M - m : kMxGemvMaxM, K, N,
+                                          static_cast<char*>(y) + m * N * 2, act, s);
+      if (e != hipSuccess) return status_of(e);
+    }
+    return WQBMM_OK;
+  }
+  const MxGemmPlan plan = act ? mx_gemm4_plan(M, K, N) : mx_gemm16_plan(M, K, N);
   uint8_t* ws = nullptr;
   st = host_workspace(dev, s, plan.x_bytes + plan.part_bytes, &ws);
   if (st != WQBMM_OK) return st;
-  return status_of(launch_mx_gemm(x, dtype, ldx, w, M, K, N, y, act, plan, ws, s));
+  return status_of(act ? launch_mx_gemm4(x, dtype, ldx, w, M, K, N, y, plan, ws, s)
+                       : launch_mx_gemm16(x, dtype, ldx, w, M, K, N, y, plan, ws, s));
 }
 
 wqbmm_status wqbmm_mxfp4_moe(const void* x, int dtype, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E,

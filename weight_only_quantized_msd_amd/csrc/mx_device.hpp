@@ -14,6 +14,7 @@ namespace wqbmm {
 
 typedef float mx_f4 __attribute__((ext_vector_type(4)));
 typedef float mx_f2 __attribute__((ext_vector_type(2)));
+typedef int mx_i4 __attribute__((ext_vector_type(4)));
 typedef int mx_i8v __attribute__((ext_vector_type(8)));
 typedef __bf16 mx_bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 mx_bf8 __attribute__((ext_vector_type(8)));
@@ -108,6 +109,22 @@ __device__ __forceinline__ uint4 mx_decode8(uint32_t c, float scale) {
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1)),
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2)),
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3)));
+  }
+}
+
+// A quarter of it: the two values of byte `part` (a constant once inlined).
+template <int DT>
+__device__ __forceinline__ uint32_t mx_decode2(uint32_t c, int part, float scale) {
+  if constexpr (DT == MX_BF16) {
+    return part == 0   ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0))
+           : part == 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1))
+           : part == 2 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2))
+                       : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+  } else {
+    return part == 0   ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 0))
+           : part == 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1))
+           : part == 2 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2))
+                       : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3));
   }
 }
 

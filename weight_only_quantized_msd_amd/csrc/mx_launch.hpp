@@ -77,18 +77,32 @@ constexpr int64_t kMxGemvMaxM = 64;
 hipError_t launch_mx_gemv(const void* x, int dtype, int64_t ldx, const MxTiled& w, int64_t M, int64_t K,
                           int64_t N, void* y, int act, hipStream_t stream);
 
-// More rows: tiled MFMA products.  ACT_MXFP4 first quantises x into a tiled
-// matrix in the workspace.
+// More rows: tiled MFMA products, of 16-bit x (mx_gemm16.hip) or of x quantised
+// into a tiled matrix in the workspace first (mx_gemm4.hip).
 struct MxGemmPlan {
-  int variant;                // workgroup tile, see mx_gemm.hip
+  int variant;                // workgroup tile, an index into the product's MxTileCost
   int64_t mblocks, nblocks;
   int64_t splits, kq_per;     // K-splits (quads of K-tiles each); > 1: fp32 partial sums + a reduction
-  size_t x_bytes, part_bytes; // workspace: tiled x (ACT_MXFP4), partial sums
+  size_t x_bytes, part_bytes; // workspace: tiled x, then the partial sums
 };
-MxGemmPlan mx_gemm_plan(int64_t M, int64_t K, int64_t N, int act);
-hipError_t launch_mx_gemm(const void* x, int dtype, int64_t ldx, const MxTiled& w, int64_t M, int64_t K,
-                          int64_t N, void* y, int act, const MxGemmPlan& plan, uint8_t* ws,
-                          hipStream_t stream);
+// A workgroup tile and what it takes: us for one K-tile (128 k) of a tile with
+// every CU busy, and `fixed` us per round of tiles (first copies, output).
+struct MxTileCost {
+  int bm, bn;
+  double fixed, per_ktile;
+};
+// The tile and split with the least estimated time: `base` us, then rounds of
+// 256 workgroups; a split adds a launch of 2 us and its partial sums' traffic.
+MxGemmPlan mx_choose(const MxTileCost* tiles, int count, double base, int64_t M, int64_t K, int64_t N);
+constexpr int64_t kMxGemmMaxLd = int64_t(1) << 22;   // rows of 16-bit x are less than this apart
+MxGemmPlan mx_gemm16_plan(int64_t M, int64_t K, int64_t N);
+MxGemmPlan mx_gemm4_plan(int64_t M, int64_t K, int64_t N);
+hipError_t launch_mx_gemm16(const void* x, int dtype, int64_t ldx, const MxTiled& w, int64_t M, int64_t K, int64_t N,
+                            void* y, const MxGemmPlan& plan, uint8_t* ws, hipStream_t stream);
+hipError_t launch_mx_gemm4(const void* x, int dtype, int64_t ldx, const MxTiled& w, int64_t M, int64_t K, int64_t N,
+                           void* y, const MxGemmPlan& plan, uint8_t* ws, hipStream_t stream);
+hipError_t launch_mx_reduce(const float* part, int splits, int64_t M, int64_t N, void* y, int dtype,
+                            hipStream_t stream);
 
 // The mixture-of-experts layer: routing, gate/up products, down product.
 constexpr int kMoeMaxT = 64;
