@@ -84,7 +84,7 @@ wqbmm_status wqbmm_mxfp4_matmul(const void* x, int dtype, int64_t ldx, const voi
   if (st != WQBMM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const MxTiled w = mx_view(w_tiled, K, N);
-  if (M <= kMxGemvMaxM) return status_of(launch_mx_gemv(x, dtype, ldx, w, M, K, N, y, act, s));
+  if (mx_use_gemv(M, K, N)) return status_of(launch_mx_gemv(x, dtype, ldx, w, M, K, N, y, act, s));
   if (!act && ldx >= kMxGemmMaxLd) {     // the tiled product addresses a tile of x with 31 bits
     for (int64_t m = 0; m < M; m += kMxGemvMaxM) {
       const hipError_t e = launch_mx_gemv(static_cast<const char*>(x) + m * ldx * 2, dtype, ldx, w,
@@ -119,7 +119,7 @@ wqbmm_status wqbmm_mxfp4_moe(const void* x, int dtype, int64_t ldx, int64_t T, i
   if (st != WQBMM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = nullptr;
-  st = host_workspace(dev, s, mx_moe_workspace_bytes(T, I, k), &ws);
+  st = host_workspace(dev, s, mx_moe_workspace_bytes(T, H, I, k), &ws);
   if (st != WQBMM_OK) return st;
   return status_of(launch_mx_moe(x, dtype, ldx, T, H, I, E, k, renormalize != 0, router, mx_view(gate_up, H, E * 2 * I),
                                  mx_view(down, I, E * H), y, topk_ids, topk_weights, ws, s));

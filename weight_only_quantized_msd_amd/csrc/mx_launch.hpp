@@ -74,6 +74,7 @@ hipError_t launch_mx_tile(const void* codes, const void* scales, int64_t K, int6
 
 // Few rows (M <= kMxGemvMaxM): one weight-streaming kernel, x read as it is.
 constexpr int64_t kMxGemvMaxM = 64;
+bool mx_use_gemv(int64_t M, int64_t K, int64_t N);
 hipError_t launch_mx_gemv(const void* x, int dtype, int64_t ldx, const MxTiled& w, int64_t M, int64_t K,
                           int64_t N, void* y, int act, hipStream_t stream);
 
@@ -108,7 +109,7 @@ hipError_t launch_mx_reduce(const float* part, int splits, int64_t M, int64_t N,
 constexpr int kMoeMaxT = 64;
 constexpr int kMoeMaxE = 256;
 constexpr int kMoeMaxK = 16;
-size_t mx_moe_workspace_bytes(int64_t T, int64_t I, int64_t k);
+size_t mx_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t k);
 hipError_t launch_mx_moe(const void* x, int dtype, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E,
                          int64_t k, bool renormalize, const void* router, const MxTiled& gate_up,
                          const MxTiled& down, void* y, int32_t* ids, float* weights, uint8_t* ws,

@@ -1,18 +1,24 @@
 // mx_moe.hip -- a mixture-of-experts layer with MXFP4 experts for up to 64
-// tokens, in three launches:
+// tokens, in four launches (three for one token):
 //   route: logits = router . x, softmax, the k largest per token;
 //   up:    h = weight * silu(gate_e . x) * (up_e . x) for every (token, choice)
-//          pair, per reached expert and panel of 16 rows of I;
-//   down:  y = sum over a token's pairs of down_e . h, per panel of 16 columns
-//          of y, over all reached experts.
-// Each reached expert's weights are read once, by the workgroups of its panels;
-// every sum has a fixed order.  There is no hand-off between workgroups inside
-// a launch: each workgroup of `up` and `down` finds its expert's pairs itself
-// from the ids (at most 1024 of them).
+//          pair, a workgroup for a reached expert and one or two panels of 16
+//          rows of I;
+//   down:  down_e . h for every pair, a workgroup for a reached expert and four
+//          panels of 16 columns of y;
+//   sum:   y = the sum of a token's pairs.
+// Each reached expert's weights are read by one workgroup a panel (once, or once
+// for every 32 of its rows); every sum has a fixed order.  There is no hand-off
+// between workgroups inside a launch: each workgroup finds its expert's pairs
+// itself from the ids (at most 1024 of them).
+//
+// Bound by the weights: 16 tokens, H = 4096, I = 11008, 8 experts, 2 chosen: route
+// 6 us, up 76 (383 MB, 5.0 TB/s), down 40 (191 MB, 4.8 TB/s), sum 4.  Small layers
+// are bound by the chain of launches and trips to memory: 33 tokens, H = 1056, I =
+// 736, 12 experts, 3 chosen: 4.6 + 7.6 + 5.7 + 2.6 us.
 #include <algorithm>
 
-#include "mx_device.hpp"
-#include "mx_launch.hpp"
+#include "mx_tile.hpp"
 
 namespace wqbmm {
 
@@ -40,132 +46,151 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // ---------------------------------------------------------------- routing
 constexpr int ROUTE_WAVES = 16;
 
-// One workgroup per token.  A wave takes experts in turn, lanes along H; wave 0
-// then picks the k largest (key, lowest index first) and forms the weights.
+// A wave's logits of N experts, lanes along H, with up to 4 * N loads of the
+// router in flight (one expert and one load at a time: 11.7 us for 1 token, 64
+// experts, H = 2048; this way, four experts a wave, 6.8).
+template <int DT, int N>
+__device__ __forceinline__ void router_logits(const uint4* __restrict__ xr, const uint16_t* __restrict__ router, int H,
+                                              int E, int e0, int lane, float (&s)[N]) {
+  constexpr int CB = 4;                         // chunks of x at a time
+  const int chunks = H / 8;
+  const uint4* rr[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rr[i] = reinterpret_cast<const uint4*>(router + (int64_t)min(e0 + i, E - 1) * H);
+    s[i] = 0.0f;
+  }
+  for (int c0 = 0; c0 < chunks; c0 += 64 * CB) {
+    uint4 a[CB], b[N][CB];
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const int c = c0 + j * 64 + lane;
+      const bool in = c < chunks;
+      a[j] = in ? xr[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) b[i][j] = in ? rr[i][c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          s[i] = __builtin_fmaf(mx_lo<DT>(dword_of(a[j], q)), mx_lo<DT>(dword_of(b[i][j], q)), s[i]);
+          s[i] = __builtin_fmaf(mx_hi<DT>(dword_of(a[j], q)), mx_hi<DT>(dword_of(b[i][j], q)), s[i]);
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
+}
+
+// The choices of one token, from its logits, by all `waves` of a workgroup: an
+// expert's rank is the number of experts ahead of it (larger logit, then lower
+// index); ranks below k are the choices, and lane j of every wave gets the j-th
+// one's index and softmax weight.
+struct Choice {
+  float logits[kMoeMaxE];
+  uint32_t keys[kMoeMaxE];
+  int rank[kMoeMaxE], chosen[kMoeMaxK];
+};
+__device__ __forceinline__ void choose(Choice& c, int E, int k, bool renormalize, int tid, int threads, int& my_id,
+                                       float& my_weight) {
+  const int lane = tid & 63, wave = tid >> 6, waves = threads >> 6;
+  for (int e = tid; e < E; e += threads) {
+    c.keys[e] = order_key(c.logits[e]);
+    c.rank[e] = 0;
+  }
+  __syncthreads();
+  const int part = (E + waves - 1) / waves, lo = wave * part, hi = min(E, lo + part);
+  for (int e = lane; e < E; e += 64) {
+    const uint32_t mine = c.keys[e];
+    int ahead = 0;
+    for (int o = lo; o < hi; ++o) {
+      const uint32_t other = c.keys[o];
+      ahead += other > mine || (other == mine && o < e);
+    }
+    if (ahead) atomicAdd(&c.rank[e], ahead);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += threads)
+    if (c.rank[e] < k) c.chosen[c.rank[e]] = e;
+  __syncthreads();
+  my_id = lane < k ? c.chosen[lane] : 0;
+  const float top = c.logits[c.chosen[0]];
+  const float mine = lane < k ? expf(c.logits[my_id] - top) : 0.0f;
+  float sum = mine;
+  if (!renormalize) {                           // over all experts instead
+    sum = 0.0f;
+    for (int e = lane; e < E; e += 64) sum += expf(c.logits[e] - top);
+  }
+  my_weight = mine / wave_sum(sum);
+}
+
+// One workgroup per token, four experts a wave at a time.
 template <int DT>
 __global__ __launch_bounds__(ROUTE_WAVES * 64) void mx_route_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                                     const uint16_t* __restrict__ router, int H,
                                                                     int E, int k, int renormalize,
                                                                     int32_t* __restrict__ ids,
                                                                     float* __restrict__ weights) {
-  __shared__ float logits[kMoeMaxE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ Choice c;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t t = blockIdx.x;
-  const uint4* xr = reinterpret_cast<const uint4*>(x + t * ldx);
-  for (int e = wave; e < E; e += ROUTE_WAVES) {
-    const uint4* rr = reinterpret_cast<const uint4*>(router + (int64_t)e * H);
-    float s = 0.0f;
-    for (int c = lane; c < H / 8; c += 64) {
-      const uint4 a = xr[c], b = rr[c];
+  constexpr int N = 4;
+  for (int e0 = wave * N; e0 < E; e0 += ROUTE_WAVES * N) {
+    float s[N];
+    router_logits<DT, N>(reinterpret_cast<const uint4*>(x + t * ldx), router, H, E, e0, lane, s);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s = __builtin_fmaf(mx_lo<DT>(dword_of(a, j)), mx_lo<DT>(dword_of(b, j)), s);
-        s = __builtin_fmaf(mx_hi<DT>(dword_of(a, j)), mx_hi<DT>(dword_of(b, j)), s);
-      }
-    }
-    s = wave_sum(s);
-    if (lane == 0) logits[e] = s;
+    for (int i = 0; i < N; ++i)
+      if (lane == 0 && e0 + i < E) c.logits[e0 + i] = s[i];
   }
   __syncthreads();
-  if (wave != 0) return;
-  constexpr int PER = kMoeMaxE / 64;
-  float v[PER];
-  uint64_t key[PER];
-  float top = 0.0f;
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < E ? logits[e] : 0.0f;
-    // larger logit first, then the lower index; 0 is below every candidate
-    key[i] = e < E ? ((uint64_t)order_key(v[i]) << 32) | (uint32_t)(0xffffffffu - e) : 0;
-  }
-  float total = 0.0f, mine = 0.0f;      // sum of the chosen; lane j holds the j-th choice
-  int my_id = 0;
-  for (int j = 0; j < k; ++j) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) best = best > key[i] ? best : key[i];
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d);
-      best = best > o ? best : o;
-    }
-    const int e = (int)(0xffffffffu - (uint32_t)best);
-    const float l = logits[e];
-    if (j == 0) top = l;
-    const float p = expf(l - top);
-    total += p;
-    if (lane == j) {
-      mine = p;
-      my_id = e;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (key[i] == best) key[i] = 0;
-  }
-  if (!renormalize) {                   // over all experts instead
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 64 * i < E) s += expf(v[i] - top);
-    total = wave_sum(s);
-  }
-  if (lane < k) {
-    ids[t * k + lane] = my_id;
-    weights[t * k + lane] = mine / total;
+  int id;
+  float weight;
+  choose(c, E, k, renormalize != 0, tid, ROUTE_WAVES * 64, id, weight);
+  if (wave == 0 && lane < k) {
+    ids[t * k + lane] = id;
+    weights[t * k + lane] = weight;
   }
 }
 
-// ---------------------------------------------------------------- up
-// The pairs (token * k + choice) of the slot-th reached expert, in ascending
-// order; returns the expert, or -1 if fewer are reached.  Every thread of the
-// workgroup calls it.  mask: 8 words, counts: one per wave, list: up to 64.
-template <int WAVES>
-__device__ __forceinline__ int pairs_of_slot(const int32_t* __restrict__ ids, int pairs, int slot, uint32_t* mask,
-                                             int* counts, uint16_t* list, int& count) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int PER = kMoeMaxT * kMoeMaxK / (WAVES * 64) > 0 ? kMoeMaxT * kMoeMaxK / (WAVES * 64) : 1;
-  if (tid < kMoeMaxE / 32) mask[tid] = 0;
-  __syncthreads();
-  int id[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int p = i * WAVES * 64 + tid;
-    id[i] = p < pairs ? ids[p] : -1;
-    if (id[i] >= 0) atomicOr(&mask[id[i] >> 5], 1u << (id[i] & 31));
-  }
-  __syncthreads();
-  int expert = -1, left = slot;
-  for (int w = 0; w < kMoeMaxE / 32; ++w) {
-    uint32_t m = mask[w];
-    const int n = __popc(m);
-    if (left < n) {
-      for (; left > 0; --left) m &= m - 1;
-      expert = 32 * w + __ffs(m) - 1;
-      break;
-    }
-    left -= n;
-  }
-  if (expert < 0) return -1;
-  int base = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const bool hit = id[i] == expert;
+// ---------------------------------------------------------------- an expert's pairs
+// Which expert a slot stands for: where there are fewer pairs (token * k +
+// choice) than experts, slot i is pair i's expert, if no pair before i has the
+// same; else slot i is expert i.  `list` (LDS of this wave's own, T entries)
+// gets the expert's pairs in ascending order.  Returns the expert, or -1 if the
+// slot is empty.  Each wave does this by itself: no barrier stands between the
+// ids and the first load of weights.
+__device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int pairs, int E, int slot, int lane,
+                                          uint16_t* list, int& count) {
+  const bool by_pair = pairs < E;
+  const int expert = by_pair ? ids[slot] : slot;
+  int n = 0;
+  bool mine = true;
+  for (int p0 = 0; p0 < pairs; p0 += 64) {
+    const int p = p0 + lane;
+    const bool hit = p < pairs && ids[p] == expert;
     const uint64_t votes = __ballot(hit);
-    if (lane == 0) counts[wave] = __popcll(votes);
-    __syncthreads();
-    int before = base;
-    for (int w = 0; w < WAVES; ++w) {
-      if (w < wave) before += counts[w];
-      base += counts[w];
-    }
-    if (hit) list[before + __popcll(votes & ((1ull << lane) - 1))] = (uint16_t)(i * WAVES * 64 + tid);
-    __syncthreads();
+    if (hit) list[n + __popcll(votes & ((1ull << lane) - 1))] = (uint16_t)p;
+    if (by_pair && n == 0 && votes != 0) mine = p0 + __ffsll((unsigned long long)votes) - 1 == slot;
+    n += __popcll(votes);
   }
-  count = base;
-  return expert;
+  count = n;
+  return n > 0 && mine ? expert : -1;
 }
 
-constexpr int UP_WAVES = 4;
+// ---------------------------------------------------------------- products
+// Both products of an expert are the same contraction: P panels of its weights
+// with the rows of its pairs (tokens' x; h), the waves of a workgroup taking
+// units of U K-tiles in turn.  The rows come in one of two ways:
+//   staged: each wave copies a unit's rows to 16 KB of LDS of its own, 1 KB of
+//     whole rows a copy, the 16-byte chunks of a row permuted (chunk ^ row % 16);
+//   direct: each lane loads its 16-byte operands, which touches a cache line a
+//     lane, but needs no LDS, so more workgroups share a CU.
+// Staged is for experts with more than a few rows (launch_mx_moe's rule).
+enum class Rows { kAsIs, kSplit, kPair };      // 16-bit; fp16 as two bf16; bf16 pairs (h)
+constexpr int STAGE_BYTES = 16 * 1024;
 
 // 16 significant bits of h: two bf16 parts, whose products with the weights
 // are exact, and which keep fp32's range (h in fp16 would overflow early, in
@@ -185,287 +210,428 @@ __device__ __forceinline__ void store_h(uint16_t* __restrict__ hi, uint16_t* __r
   *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
 }
 
-template <int DT, bool SPLIT, int MT>
-__device__ __forceinline__ void up_quads(const uint16_t* __restrict__ x, int64_t ldx, const MxTiled& w,
-                                         int64_t gate_panel, int64_t up_panel, const uint16_t* list, int count, int k,
-                                         int blocks, int wave, int lane, mx_f4 (&acc)[2][MT]) {
+// h's rows, one for each pair, hold whole K-tiles (what lies past I is not used).
+__host__ __device__ inline int64_t h_pitch(int64_t I) { return (I + 127) / 128 * 128; }
+
+// Where h's value i of a row stands.  Within a K-tile of 128 values the 16-byte
+// chunks are ordered (slice j, block g) instead of (g, j): the four lanes that
+// read a row's slice j then read 64 bytes in a row.
+__device__ __forceinline__ int h_place(int i) {
+  return (i & ~127) | ((i & 24) << 2) | ((i & 96) >> 2) | (i & 7);
+}
+
+// row_at(i): the first value of row i, as an offset into `src` (and `src_lo`).
+template <int DT, Rows MODE, int MT, int P, bool STAGED, typename RowAt>
+__device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
+                                             RowAt&& row_at, const MxTiled& w, const int64_t (&panel)[P], int rows,
+                                             int blocks, int wave, int waves, int lane, uint8_t* xs,
+                                             mx_f4 (&acc)[P][MT]) {
+  constexpr bool PAIR = MODE == Rows::kPair;
+  constexpr int U = STAGED ? (PAIR ? 2 : 4) / MT : 4;
+  constexpr int LANES = 16 * U, ROWS = 64 / LANES, LO = STAGE_BYTES / 2;
+  constexpr int CT = MODE == Rows::kAsIs ? DT : MX_BF16;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t panel[2] = {gate_panel, up_panel};
-  int64_t row[MT];
+  auto chunk_of = [&](int i, int j) __attribute__((always_inline)) { return PAIR ? 16 * i + 4 * j + g : 16 * i + 4 * g + j; };
+  for (int kt = wave * U; kt < w.kt; kt += waves * U) {
+    if constexpr (STAGED) {
+      mx_wait_lds();                              // the last unit's reads, before its rows are overwritten
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-    row[mt] = mt * 16 + r < count ? (int64_t)(list[mt * 16 + r] / k) * ldx : -1;
-  for (int q = wave; q < w.kq; q += UP_WAVES) {
-    uint4 c[2][4];
-    uint32_t sc[2];
+      for (int i = 0; i < 16 * MT / ROWS; ++i) {
+        if (i * ROWS >= rows) break;
+        const int row = i * ROWS + lane / LANES;
+        const int chunk = kt * 16 + ((lane % LANES) ^ (row & 15));
+        const bool in = chunk < (PAIR ? w.kt * 16 : blocks * 4);
+        const int64_t at = row_at(min(row, rows - 1)) + (in ? chunk * 8 : 0);
+        __builtin_amdgcn_global_load_lds(src + at, xs + i * 1024, 16, 0, 0);
+        if constexpr (PAIR) __builtin_amdgcn_global_load_lds(src_lo + at, xs + LO + i * 1024, 16, 0, 0);
+      }
+    }
+    uint4 c[P][U];
+    uint32_t sc[P];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < P; ++p) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[p][i] = *reinterpret_cast<const uint4*>(
-            w.codes + ((panel[p] * w.kt + min(4 * q + i, w.kt - 1)) * 64 + lane) * 16);
-      sc[p] = *reinterpret_cast<const uint32_t*>(w.scales + ((panel[p] * w.kq + q) * 64 + lane) * 4);
+      for (int i = 0; i < U; ++i)
+        c[p][i] = *reinterpret_cast<const uint4*>(w.codes + ((panel[p] * w.kt + min(kt + i, w.kt - 1)) * 64 + lane) * 16);
+      sc[p] = *reinterpret_cast<const uint32_t*>(w.scales + ((panel[p] * w.kq + kt / 4) * 64 + lane) * 4) >> (8 * (kt & 3));
+    }
+    if constexpr (STAGED) mx_wait_vm<0>();
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (kt + i >= w.kt) break;                  // uniform: the last unit's missing tiles
+      const bool whole = 4 * (kt + i) + 4 <= blocks, in = 4 * (kt + i) + g < blocks;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint4 v[4], l[4];
+        if constexpr (STAGED) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint8_t* const at = xs + (mt * 16 + r) * (LANES * 16) + (chunk_of(i, j) ^ r) * 16;
+            v[j] = *reinterpret_cast<const uint4*>(at);
+            if constexpr (PAIR) l[j] = *reinterpret_cast<const uint4*>(at + LO);
+          }
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = in ? v[j] : make_uint4(0u, 0u, 0u, 0u);
+              if constexpr (PAIR) l[j] = in ? l[j] : make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = l[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (mt * 16 + r < rows && in) {
+            const int64_t at = row_at(mt * 16 + r) + kt * kMxTile;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = *reinterpret_cast<const uint4*>(src + at + chunk_of(i, j) * 8);
+              if constexpr (PAIR) l[j] = *reinterpret_cast<const uint4*>(src_lo + at + chunk_of(i, j) * 8);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (MODE == Rows::kSplit) {
+            const uint4 both = v[j];
+            mx_split8(both, v[j], l[j]);
+          }
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint4 a = mx_decode8<CT>(dword_of(c[p][i], j), mx_scale((sc[p] >> (8 * i)) & 0xffu));
+            acc[p][mt] = mx_mfma16<CT>(a, v[j], acc[p][mt]);
+            if constexpr (MODE != Rows::kAsIs) acc[p][mt] = mx_mfma16<CT>(a, l[j], acc[p][mt]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The waves' sums -> part [wave][P * MT][64]; call with all waves, after which
+// total(i) adds sum i of the P * MT over the waves, in wave order.
+template <int P, int MT>
+__device__ __forceinline__ void share_sums(mx_f4* part, const mx_f4 (&acc)[P][MT], int wave, int lane) {
+  __syncthreads();                                // the staged rows lie in the same memory
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) part[(wave * P * MT + p * MT + mt) * 64 + lane] = acc[p][mt];
+  __syncthreads();
+}
+template <int P, int MT>
+__device__ __forceinline__ mx_f4 total(const mx_f4* part, int i, int waves, int lane) {
+  mx_f4 v = part[i * 64 + lane];
+  for (int s = 1; s < waves; ++s) v += part[(s * P * MT + i) * 64 + lane];
+  return v;
+}
+
+// h of `rows` pairs from `first` on, for Q panels of 16 rows of I; UP_WAVES waves.
+constexpr int UP_WAVES = 4;
+template <int DT, int MT, int Q, typename RowAt, typename PairOf, typename ShareOf>
+__device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& row_at, PairOf&& pair_of,
+                                        ShareOf&& share_of, const MxTiled& w, int expert, int rows, int blocks, int I,
+                                        int wave, int lane, mx_f4* part, uint16_t* __restrict__ h_hi,
+                                        uint16_t* __restrict__ h_lo) {
+  constexpr int P = 2 * Q;                        // gate panels, then up panels
+  int64_t panel[P];
+  uint32_t f16 = kMxFlagF16;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    panel[q] = (int64_t)expert * (2 * I / kMxPanel) + min((int)blockIdx.x * Q + q, I / kMxPanel - 1);
+    panel[Q + q] = panel[q] + I / kMxPanel;
+    if (DT == MX_F16) f16 &= w.flags[panel[q]] & w.flags[panel[Q + q]];
+  }
+  mx_f4 acc[P][MT];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
+  if (DT == MX_BF16 || f16)
+    expert_units<DT, Rows::kAsIs, MT, P, false>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, nullptr, acc);
+  else
+    expert_units<DT, Rows::kSplit, MT, P, false>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, nullptr, acc);
+  share_sums<P, MT>(part, acc, wave, lane);
+  for (int qm = wave; qm < Q * MT; qm += UP_WAVES) {
+    const int i = qm % MT * 16 + (lane & 15);
+    const int at = (blockIdx.x * Q + qm / MT) * kMxPanel + 4 * (lane >> 4);
+    if (i >= rows || at >= I) continue;
+    const mx_f4 a = total<P, MT>(part, qm, UP_WAVES, lane), b = total<P, MT>(part, Q * MT + qm, UP_WAVES, lane);
+    const float share = share_of(i);
+    mx_f4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = a[j] / (1.0f + expf(-a[j])) * b[j] * share;
+    store_h(h_hi, h_lo, pair_of(i) * h_pitch(I) + h_place(at), h);
+  }
+}
+
+// Workgroup (Q panels of 16 rows of I, slot): h for all pairs of the slot's expert.
+template <int DT, int Q>
+__global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                                 MxTiled w, const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ weights, int pairs, int E,
+                                                                 int k, int blocks, int I,
+                                                                 uint16_t* __restrict__ h_hi,
+                                                                 uint16_t* __restrict__ h_lo) {
+  __shared__ mx_f4 part[UP_WAVES * 4 * Q * 64];
+  __shared__ uint16_t lists[UP_WAVES][kMoeMaxT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t* const list = lists[wave];
+  int count = 0;
+  const int expert = __builtin_amdgcn_readfirstlane(slot_pairs(ids, pairs, E, blockIdx.y, lane, list, count));
+  if (expert < 0) return;                         // all waves find the same
+  count = __builtin_amdgcn_readfirstlane(count);
+  auto rows_from = [&](auto mt_c, int first) __attribute__((always_inline)) {
+    constexpr int MT = decltype(mt_c)::value;
+    up_rows<DT, MT, Q>(
+        x, [&](int i) __attribute__((always_inline)) { return (int64_t)(list[first + i] / k) * ldx; },
+        [&](int i) __attribute__((always_inline)) { return (int)list[first + i]; },
+        [&](int i) __attribute__((always_inline)) { return weights[list[first + i]]; }, w, expert,
+        min(count - first, MT * 16), blocks, I, wave, lane, part, h_hi, h_lo);
+  };
+  int first = 0;
+  for (; count - first > 16; first += 32) {
+    rows_from(std::integral_constant<int, 2>{}, first);
+    __syncthreads();                              // the sums are read before they are overwritten
+  }
+  if (first < count) rows_from(std::integral_constant<int, 1>{}, first);
+}
+
+// Workgroup (P panels of 16 columns of y, slot): the expert's share of y, fp32,
+// for each of its pairs.
+template <int P, bool STAGED>
+__global__ __launch_bounds__(STAGED ? 512 : 256) void mx_moe_down_kernel(const uint16_t* __restrict__ h_hi,
+                                                                        const uint16_t* __restrict__ h_lo, MxTiled w,
+                                                                        const int32_t* __restrict__ ids, int pairs,
+                                                                        int E, int I, int H,
+                                                                        float* __restrict__ sums) {
+  constexpr int WAVES = STAGED ? 8 : 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGED ? WAVES * STAGE_BYTES : WAVES * 2 * P * 1024];
+  __shared__ uint16_t lists[WAVES][kMoeMaxT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t* const list = lists[wave];
+  mx_f4* const part = reinterpret_cast<mx_f4*>(lds);
+  int count = 0;
+  const int expert = __builtin_amdgcn_readfirstlane(slot_pairs(ids, pairs, E, blockIdx.y, lane, list, count));
+  if (expert < 0) return;
+  count = __builtin_amdgcn_readfirstlane(count);
+  int64_t panel[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    panel[p] = (int64_t)expert * (H / kMxPanel) + min((int)blockIdx.x * P + p, H / kMxPanel - 1);
+
+  auto rows_from = [&](auto mt_c, int first) __attribute__((always_inline)) {
+    constexpr int MT = decltype(mt_c)::value;
+    const int rows = min(count - first, MT * 16);
+    auto row_at = [&](int i) __attribute__((always_inline)) { return list[first + i] * h_pitch(I); };
+    mx_f4 acc[P][MT];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
+    expert_units<MX_BF16, Rows::kPair, MT, P, STAGED>(h_hi, h_lo, row_at, w, panel, rows, I / kMxBlock, wave, WAVES,
+                                                      lane, lds + wave * STAGE_BYTES, acc);
+    share_sums<P, MT>(part, acc, wave, lane);
+    for (int pm = wave; pm < P * MT; pm += WAVES) {
+      const int i = pm % MT * 16 + (lane & 15);
+      const int n = (blockIdx.x * P + pm / MT) * kMxPanel + 4 * (lane >> 4);
+      const mx_f4 v = total<P, MT>(part, pm, WAVES, lane);
+      if (i < rows && n < H) *reinterpret_cast<mx_f4*>(sums + (int64_t)list[first + i] * H + n) = v;
+    }
+  };
+  int first = 0;
+  for (; count - first > 16; first += 32) {
+    rows_from(std::integral_constant<int, 2>{}, first);
+    __syncthreads();
+  }
+  if (first < count) rows_from(std::integral_constant<int, 1>{}, first);
+}
+
+// y[t] = the sum of token t's pairs, in order of choice; a thread takes four columns.
+template <int DT>
+__global__ __launch_bounds__(256) void mx_moe_sum_kernel(const float* __restrict__ sums, int k, uint32_t units,
+                                                         int64_t count, uint16_t* __restrict__ y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;            // of count = T * units
+  if (i >= count) return;
+  const int64_t t = i / units, c = i - t * units;
+  const mx_f4* const from = reinterpret_cast<const mx_f4*>(sums) + t * k * units + c;
+  mx_f4 v = from[0];
+#pragma unroll 4
+  for (int j = 1; j < k; ++j) v += from[j * (int64_t)units];
+  reinterpret_cast<uint2*>(y)[i] = mx_pack4<DT>(v);
+}
+
+// ---------------------------------------------------------------- one token
+// Its choices are the k slots.  The logits come from many workgroups (a single
+// one reads the router at some 100 GB/s), each workgroup of the gate and up
+// product then chooses by itself, and one workgroup adds all experts' shares of
+// its columns of y.
+template <int DT>
+__global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __restrict__ x,
+                                                            const uint16_t* __restrict__ router, int H, int E,
+                                                            float* __restrict__ logits) {
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float s[1];
+  router_logits<DT, 1>(reinterpret_cast<const uint4*>(x), router, H, E, e, lane, s);
+  if (lane == 0 && e < E) logits[e] = s[0];
+}
+
+template <int DT>
+__global__ __launch_bounds__(UP_WAVES * 64) void mx_one_up_kernel(const uint16_t* __restrict__ x, MxTiled w,
+                                                                 const float* __restrict__ logits, int E, int k,
+                                                                 int renormalize, int blocks, int I,
+                                                                 int32_t* __restrict__ ids,
+                                                                 float* __restrict__ weights,
+                                                                 uint16_t* __restrict__ h_hi,
+                                                                 uint16_t* __restrict__ h_lo) {
+  __shared__ mx_f4 part[UP_WAVES * 2 * 64];
+  __shared__ Choice c;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int e = tid; e < E; e += UP_WAVES * 64) c.logits[e] = logits[e];
+  __syncthreads();
+  int id;
+  float weight;
+  choose(c, E, k, renormalize != 0, tid, UP_WAVES * 64, id, weight);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0 && lane < k) {
+    ids[lane] = id;
+    weights[lane] = weight;
+  }
+  const int slot = blockIdx.y, expert = __builtin_amdgcn_readfirstlane(__shfl(id, slot));
+  const float share = __shfl(weight, slot);
+  up_rows<DT, 1, 1>(
+      x, [](int) __attribute__((always_inline)) { return (int64_t)0; },
+      [&](int) __attribute__((always_inline)) { return slot; },
+      [&](int) __attribute__((always_inline)) { return share; }, w, expert, 1, blocks, I, wave, lane, part, h_hi, h_lo);
+}
+
+// Workgroup: a panel of 16 columns of y.  A unit is a choice's quad of K-tiles;
+// the next unit's codes are loaded while the present one is multiplied.
+constexpr int ONE_WAVES = 8;
+template <int DT>
+__global__ __launch_bounds__(ONE_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h_hi,
+                                                                    const uint16_t* __restrict__ h_lo, MxTiled w,
+                                                                    const int32_t* __restrict__ ids, int k, int I,
+                                                                    int H, uint16_t* __restrict__ y) {
+  __shared__ mx_f4 part[ONE_WAVES * 64];
+  const int lane = threadIdx.x & 63, g = lane >> 4, blocks = I / kMxBlock;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int units = k * w.kq;
+  mx_f4 acc[1][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}};
+  uint4 c[4], next[4];
+  uint32_t sc = 0, sc_next = 0;
+  auto load = [&](int u, uint4 (&to)[4], uint32_t& s) __attribute__((always_inline)) {
+    const int q = u % w.kq;
+    const int64_t panel = (int64_t)ids[u / w.kq] * (H / kMxPanel) + blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      to[i] = *reinterpret_cast<const uint4*>(w.codes + ((panel * w.kt + min(4 * q + i, w.kt - 1)) * 64 + lane) * 16);
+    s = *reinterpret_cast<const uint32_t*>(w.scales + ((panel * w.kq + q) * 64 + lane) * 4);
+  };
+  if (wave < units) load(wave, c, sc);
+  for (int u = wave; u < units; u += ONE_WAVES) {
+    if (u + ONE_WAVES < units) load(u + ONE_WAVES, next, sc_next);
+    const int q = u % w.kq;
+    const int64_t row = u / w.kq * h_pitch(I);
+    uint4 v[4][4] = {}, l[4][4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((lane & 15) == 0 && 4 * (4 * q + i) + g < blocks) {
+        const int64_t at = row + (4 * q + i) * kMxTile + g * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i][j] = *reinterpret_cast<const uint4*>(h_hi + at + j * 32);
+          l[i][j] = *reinterpret_cast<const uint4*>(h_lo + at + j * 32);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (4 * q + i >= w.kt) break;
-      const int b = 4 * (4 * q + i) + g;
+      const float f = mx_scale((sc >> (8 * i)) & 0xffu);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (mt * 16 >= count) break;
-        uint4 xv[4] = {};
-        if (row[mt] >= 0 && b < blocks) {
-          const uint4* src = reinterpret_cast<const uint4*>(x + row[mt] + (int64_t)b * kMxBlock);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) xv[j] = src[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 hi, lo;
-          if constexpr (SPLIT) mx_split8(xv[j], hi, lo);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const float f = mx_scale((sc[p] >> (8 * i)) & 0xffu);
-            if constexpr (SPLIT) {
-              const uint4 a = mx_decode8<MX_BF16>(dword_of(c[p][i], j), f);
-              acc[p][mt] = mx_mfma16<MX_BF16>(a, hi, acc[p][mt]);
-              acc[p][mt] = mx_mfma16<MX_BF16>(a, lo, acc[p][mt]);
-            } else {
-              acc[p][mt] = mx_mfma16<DT>(mx_decode8<DT>(dword_of(c[p][i], j), f), xv[j], acc[p][mt]);
-            }
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        const uint4 a = mx_decode8<MX_BF16>(dword_of(c[i], j), f);
+        acc[0][0] = mx_mfma16<MX_BF16>(a, v[i][j], acc[0][0]);
+        acc[0][0] = mx_mfma16<MX_BF16>(a, l[i][j], acc[0][0]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = next[i];
+    sc = sc_next;
   }
-}
-
-// Workgroup (panel of 16 rows of I, slot): the gate panel and the up panel of
-// the slot's expert for all of its pairs; the waves split H.
-template <int DT, int MT>
-__global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                                 MxTiled w, const int32_t* __restrict__ ids,
-                                                                 const float* __restrict__ weights, int pairs, int k,
-                                                                 int blocks, int I, uint16_t* __restrict__ h_hi,
-                                                                 uint16_t* __restrict__ h_lo) {
-  __shared__ uint32_t mask[kMoeMaxE / 32];
-  __shared__ int counts[UP_WAVES];
-  __shared__ uint16_t list[kMoeMaxT];
-  __shared__ mx_f4 part[UP_WAVES][2 * MT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int count = 0;
-  const int expert = __builtin_amdgcn_readfirstlane(
-      pairs_of_slot<UP_WAVES>(ids, pairs, blockIdx.y, mask, counts, list, count));
-  if (expert < 0) return;
-  count = __builtin_amdgcn_readfirstlane(count);
-  const int64_t gate = (int64_t)expert * (2 * I / kMxPanel) + blockIdx.x, up = gate + I / kMxPanel;
-  mx_f4 acc[2][MT];
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
-  if constexpr (DT == MX_BF16) {
-    up_quads<DT, false, MT>(x, ldx, w, gate, up, list, count, k, blocks, wave, lane, acc);
-  } else {
-    if (w.flags[gate] & w.flags[up] & kMxFlagF16)
-      up_quads<DT, false, MT>(x, ldx, w, gate, up, list, count, k, blocks, wave, lane, acc);
-    else
-      up_quads<DT, true, MT>(x, ldx, w, gate, up, list, count, k, blocks, wave, lane, acc);
-  }
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) part[wave][p * MT + mt][lane] = acc[p][mt];
-  __syncthreads();
-  for (int mt = wave; mt < MT; mt += UP_WAVES) {
-    const int i = mt * 16 + (lane & 15);
-    if (i >= count) continue;
-    mx_f4 a = part[0][mt][lane], b = part[0][MT + mt][lane];
-#pragma unroll
-    for (int s = 1; s < UP_WAVES; ++s) {
-      a += part[s][mt][lane];
-      b += part[s][MT + mt][lane];
-    }
-    const int pair = list[i];
-    const float share = weights[pair];
-    mx_f4 h;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = a[j] / (1.0f + expf(-a[j])) * b[j] * share;
-    store_h(h_hi, h_lo, (int64_t)pair * I + blockIdx.x * kMxPanel + 4 * (lane >> 4), h);
-  }
-}
-
-// ---------------------------------------------------------------- down
-constexpr int DOWN_WAVES = 8;
-
-// Workgroup: one panel of 16 columns of y, all reached experts.  Pairs are
-// sorted by expert in LDS; a wave takes (expert, K range) items in turn and adds
-// each item's products to its own sums per token, which are added over the
-// waves at the end.
-template <int DT, int MT>
-__global__ __launch_bounds__(DOWN_WAVES * 64) void mx_moe_down_kernel(const uint16_t* __restrict__ h_hi,
-                                                                     const uint16_t* __restrict__ h_lo, MxTiled w,
-                                                                     const int32_t* __restrict__ ids, int T, int k,
-                                                                     int I, int H, uint16_t* __restrict__ y) {
-  constexpr int TOKENS = MT * 16;
-  __shared__ int start[kMoeMaxE + 1];             // first sorted pair of each expert
-  __shared__ int fill[kMoeMaxE];
-  __shared__ uint16_t sorted[kMoeMaxT * kMoeMaxK];
-  __shared__ uint16_t reached[kMoeMaxE];          // the reached experts, ascending
-  __shared__ int n_reached;
-  __shared__ mx_f4 sums[DOWN_WAVES][TOKENS][4];   // [wave][token][16 columns]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pairs = T * k;
-  constexpr int THREADS = DOWN_WAVES * 64;
-  constexpr int PER = kMoeMaxT * kMoeMaxK / THREADS;
-  if (tid < kMoeMaxE) fill[tid] = 0;
-  for (int i = tid; i < DOWN_WAVES * TOKENS * 4; i += THREADS) (&sums[0][0][0])[i] = mx_f4{0.f, 0.f, 0.f, 0.f};
-  __syncthreads();
-  int id[PER], rank[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int p = i * THREADS + tid;
-    id[i] = p < pairs ? ids[p] : -1;
-    if (id[i] >= 0) rank[i] = atomicAdd(&fill[id[i]], 1);
-  }
-  __syncthreads();
-  if (wave == 0) {                                // prefix sums of counts and of "reached"
-    int base = 0, seen = 0;
-    for (int i = 0; i < kMoeMaxE / 64; ++i) {
-      const int c = fill[64 * i + lane];
-      int s = c;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(s, d);
-        if (lane >= d) s += o;
-      }
-      start[64 * i + lane] = base + s - c;
-      const uint64_t votes = __ballot(c > 0);
-      if (c > 0) reached[seen + __popcll(votes & ((1ull << lane) - 1))] = (uint16_t)(64 * i + lane);
-      seen += __popcll(votes);
-      base += __shfl(s, 63);
-    }
-    if (lane == 0) {
-      start[kMoeMaxE] = base;
-      n_reached = seen;
-    }
-  }
-  __syncthreads();
-  // The order of an expert's pairs only places them in columns of the product;
-  // each sum's order does not depend on it.
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (id[i] >= 0) sorted[start[id[i]] + rank[i]] = (uint16_t)(i * THREADS + tid);
-  __syncthreads();
-
-  const int slots = __builtin_amdgcn_readfirstlane(n_reached);
-  const int parts = min(w.kq, max(1, (DOWN_WAVES + slots - 1) / slots));   // K ranges per expert
-  const int per = (w.kq + parts - 1) / parts;
-  const int r = lane & 15, g = lane >> 4, blocks = I / kMxBlock;
-  for (int item = wave; item < slots * parts; item += DOWN_WAVES) {
-    const int e = __builtin_amdgcn_readfirstlane(reached[item / parts]);
-    const int q_lo = item % parts * per, q_hi = min(w.kq, q_lo + per);
-    const int first = __builtin_amdgcn_readfirstlane(start[e]);
-    const int count = __builtin_amdgcn_readfirstlane(start[e + 1]) - first;
-    const int64_t panel = (int64_t)e * (H / kMxPanel) + blockIdx.x;
-    int pair[MT];
-    mx_f4 acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      pair[mt] = mt * 16 + r < count ? sorted[first + mt * 16 + r] : -1;
-      acc[mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
-    }
-    for (int q = q_lo; q < q_hi; ++q) {
-      uint4 c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[i] = *reinterpret_cast<const uint4*>(
-            w.codes + ((panel * w.kt + min(4 * q + i, w.kt - 1)) * 64 + lane) * 16);
-      const uint32_t sc = *reinterpret_cast<const uint32_t*>(w.scales + ((panel * w.kq + q) * 64 + lane) * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (4 * q + i >= w.kt) break;
-        const int b = 4 * (4 * q + i) + g;
-        const float f = mx_scale((sc >> (8 * i)) & 0xffu);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if (mt * 16 >= count) break;
-          uint4 hi[4] = {}, lo[4] = {};
-          if (pair[mt] >= 0 && b < blocks) {
-            const int64_t at = (int64_t)pair[mt] * I + (int64_t)b * kMxBlock;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              hi[j] = reinterpret_cast<const uint4*>(h_hi + at)[j];
-              lo[j] = reinterpret_cast<const uint4*>(h_lo + at)[j];
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 a = mx_decode8<MX_BF16>(dword_of(c[i], j), f);
-            acc[mt] = mx_mfma16<MX_BF16>(a, hi[j], acc[mt]);
-            acc[mt] = mx_mfma16<MX_BF16>(a, lo[j], acc[mt]);
-          }
-        }
-      }
-    }
-    // an expert's pairs belong to different tokens: no two lanes meet here; a
-    // token's earlier items may have been other lanes' (one wave, LDS in order)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      if (pair[mt] >= 0) sums[wave][pair[mt] / k][g] += acc[mt];
-  }
-  __syncthreads();
-  for (int i = tid; i < T * 4; i += THREADS) {
-    const int t = i >> 2, j = i & 3;
-    mx_f4 v = sums[0][t][j];
-#pragma unroll
-    for (int s = 1; s < DOWN_WAVES; ++s) v += sums[s][t][j];
-    const uint32_t lo = mx_round16<DT>(v[0]) | ((uint32_t)mx_round16<DT>(v[1]) << 16);
-    const uint32_t hi = mx_round16<DT>(v[2]) | ((uint32_t)mx_round16<DT>(v[3]) << 16);
-    *reinterpret_cast<uint2*>(y + (int64_t)t * H + blockIdx.x * kMxPanel + 4 * j) = make_uint2(lo, hi);
-  }
+  share_sums<1, 1>(part, acc, wave, lane);
+  if (wave == 0 && (lane & 15) == 0)
+    *reinterpret_cast<uint2*>(y + blockIdx.x * kMxPanel + 4 * g) = mx_pack4<DT>(total<1, 1>(part, 0, ONE_WAVES, lane));
 }
 
 // ---------------------------------------------------------------- launches
-static size_t h_bytes(int64_t T, int64_t I, int64_t k) { return (size_t)(T * k * I * 2 + 255) / 256 * 256; }
+static size_t h_bytes(int64_t T, int64_t I, int64_t k) { return (size_t)(T * k * h_pitch(I) * 2); }
 
-size_t mx_moe_workspace_bytes(int64_t T, int64_t I, int64_t k) { return 2 * h_bytes(T, I, k); }
-
-template <int DT, int MT>
-static hipError_t moe_mt(const uint16_t* x, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
-                         int renorm, const uint16_t* router, const MxTiled& gate_up, const MxTiled& down, uint16_t* y,
-                         int32_t* ids, float* weights, uint8_t* ws, hipStream_t stream) {
-  const int h = (int)H, i = (int)I, e = (int)E, kk = (int)k, t = (int)T, pairs = t * kk;
-  const int h_blocks = h / kMxBlock;
-  auto* hi = reinterpret_cast<uint16_t*>(ws);
-  auto* lo = reinterpret_cast<uint16_t*>(ws + h_bytes(T, I, k));
-  auto* cids = static_cast<const int32_t*>(ids);
-  auto* cweights = static_cast<const float*>(weights);
-  auto* chi = static_cast<const uint16_t*>(hi);
-  auto* clo = static_cast<const uint16_t*>(lo);
-  hipError_t err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, x, ldx, router, h,
-                             e, kk, renorm, ids, weights);
-  if (err != hipSuccess) return err;
-  const dim3 up_grid((unsigned)(I / kMxPanel), (unsigned)std::min<int64_t>(E, pairs));
-  err = mx_launch(mx_moe_up_kernel<DT, MT>, up_grid, dim3(UP_WAVES * 64), stream, x, ldx, gate_up, cids, cweights,
-                  pairs, kk, h_blocks, i, hi, lo);
-  if (err != hipSuccess) return err;
-  return mx_launch(mx_moe_down_kernel<DT, MT>, dim3((unsigned)(H / kMxPanel)), dim3(DOWN_WAVES * 64), stream, chi, clo,
-                   down, cids, t, kk, i, h, y);
+// h in two parts, then the pairs' shares of y (more than one token) or the logits (one).
+size_t mx_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t k) {
+  return 2 * h_bytes(T, I, k) + (T == 1 ? kMoeMaxE * 4 : (size_t)(T * k * H * 4));
 }
 
 template <int DT>
 static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renorm,
                          const void* router, const MxTiled& gate_up, const MxTiled& down, void* y, int32_t* ids,
                          float* weights, uint8_t* ws, hipStream_t stream) {
+  const int h = (int)H, i = (int)I, e = (int)E, kk = (int)k, pairs = (int)(T * k), h_blocks = h / kMxBlock;
   auto* xp = static_cast<const uint16_t*>(x);
   auto* rp = static_cast<const uint16_t*>(router);
   auto* yp = static_cast<uint16_t*>(y);
-  auto* run = T <= 16 ? moe_mt<DT, 1> : T <= 32 ? moe_mt<DT, 2> : moe_mt<DT, 4>;
-  return run(xp, ldx, T, H, I, E, k, renorm, rp, gate_up, down, yp, ids, weights, ws, stream);
+  auto* hi = reinterpret_cast<uint16_t*>(ws);
+  auto* lo = reinterpret_cast<uint16_t*>(ws + h_bytes(T, I, k));
+  auto* sums = reinterpret_cast<float*>(ws + 2 * h_bytes(T, I, k));
+  auto* chi = static_cast<const uint16_t*>(hi);
+  auto* clo = static_cast<const uint16_t*>(lo);
+  auto* cids = static_cast<const int32_t*>(ids);
+  auto* cweights = static_cast<const float*>(weights);
+  auto* csums = static_cast<const float*>(sums);
+  const unsigned rows = (unsigned)(I / kMxPanel), panels = (unsigned)(H / kMxPanel);
+  hipError_t err;
+  if (T == 1) {
+    err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4)), dim3(256), stream, xp, rp, h, e, sums);
+    if (err != hipSuccess) return err;
+    err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k), dim3(UP_WAVES * 64), stream, xp, gate_up, csums, e,
+                    kk, renorm, h_blocks, i, ids, weights, hi, lo);
+    if (err != hipSuccess) return err;
+    return mx_launch(mx_one_down_kernel<DT>, dim3(panels), dim3(ONE_WAVES * 64), stream, chi, clo, down, cids, kk, i, h,
+                     yp);
+  }
+  err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, xp, ldx, rp, h, e, kk,
+                  renorm, ids, weights);
+  if (err != hipSuccess) return err;
+  const unsigned slots = (unsigned)std::min<int64_t>(E, pairs);
+  auto up = [&](auto* kernel, unsigned q) {
+    return mx_launch(kernel, dim3((rows + q - 1) / q, slots), dim3(UP_WAVES * 64), stream, xp, ldx, gate_up, cids,
+                     cweights, pairs, e, kk, h_blocks, i, hi, lo);
+  };
+  // two pairs of panels halve the loads of x, which count from about 16 rows an
+  // expert (us of the layer with one and two: 32 x 2048 x 2048, 16 experts, 8 of
+  // them chosen 57 and 52; 33 x 1056 x 736, 12, 3: 20.9 and 21.6)
+  err = T * k >= 16 * E ? up(mx_moe_up_kernel<DT, 2>, 2) : up(mx_moe_up_kernel<DT, 1>, 1);
+  if (err != hipSuccess) return err;
+  auto go = [&](auto* kernel, unsigned p, unsigned threads) {
+    return mx_launch(kernel, dim3((panels + p - 1) / p, slots), dim3(threads), stream, chi, clo, down, cids, pairs, e, i,
+                     h, sums);
+  };
+  // Four panels share the loads of h.  Staged rows pay where eight waves of 256 k
+  // have work each, or where the workgroups make one round at most (us of the
+  // layer, direct and staged: 16 x 4096 x 11008, 8, 2: 136 and 129; 33 x 1056 x 736,
+  // 12, 3: 21.7 and 20.6; but 64 x 2048 x 1024, 64, 8: 92 and 102).  Two panels where
+  // four leave fewer than 1024 workgroups.
+  const unsigned quads = (panels + 3) / 4 * slots;
+  if (I >= 2048 || quads <= 256) err = go(mx_moe_down_kernel<4, true>, 4, 512);
+  else if (quads >= 1024) err = go(mx_moe_down_kernel<4, false>, 4, 256);
+  else err = go(mx_moe_down_kernel<2, false>, 2, 256);
+  if (err != hipSuccess) return err;
+  const uint32_t units = (uint32_t)(H / 4);
+  const int64_t n = T * units;
+  return mx_launch(mx_moe_sum_kernel<DT>, dim3((unsigned)((n + 255) / 256)), dim3(256), stream, csums, kk, units, n, yp);
 }
 
 hipError_t launch_mx_moe(const void* x, int dtype, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
