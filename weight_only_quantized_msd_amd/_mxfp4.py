@@ -2,7 +2,10 @@
 
 They check tensor metadata, allocate outputs and pass device pointers and the
 HIP stream; everything else happens in the kernels.  The calls are short
-(several run in a few microseconds), so the wrappers do as little as they can.
+(several run in a few microseconds), so the ordinary one, which allocates its
+outputs on the current stream of the current device, is made in C++
+(csrc/mx_torch.cpp, the module _mx_calls); what that hands back undone takes the
+way below, which also says what is wrong with a call.
 
 Format: 32 consecutive values along the last dimension share a scale byte s
 that stands for 2^(s - 127) (255: NaN); two 4-bit elements to a byte, the lower
@@ -15,17 +18,23 @@ from ._lib import WQBMM_ERR_INVALID, check, lib
 
 _ACTS = {"16bit": _lib.WQBMM_MXFP4_ACT_16BIT, "mxfp4": _lib.WQBMM_MXFP4_ACT_MXFP4}
 _torch = None            # torch and what is looked up in it once, set by _load
+_calls = None            # csrc/mx_torch.cpp
 _dtypes = {}
 _device_now = _raw_stream = None
 
 
 def _load():
-    global _torch, _device_now, _raw_stream
+    global _torch, _device_now, _raw_stream, _calls
     import torch
+    lib()
+    try:
+        from . import _mx_calls
+    except ImportError as e:
+        raise RuntimeError("_mx_calls.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'`") from e
     _dtypes.update({torch.float16: _lib.WQBMM_DTYPE_F16, torch.bfloat16: _lib.WQBMM_DTYPE_BF16,
                     torch.float32: _lib.WQBMM_DTYPE_F32})
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _torch = torch
+    _torch, _calls = torch, _mx_calls
     return torch
 
 
@@ -76,6 +85,10 @@ def wqbmm_mxfp4_quantize(x, codes=None, scales=None, stream=None):
     divided by it, rounded half to even and clipped at 6.  A block with an
     infinity or a NaN reads back as NaN."""
     torch = _torch or _load()
+    if codes is None and scales is None and stream is None:
+        both = _calls.quantize(x)
+        if both is not None:
+            return both
     M, K, ld = _rows(x, "x")
     code = _dtype_code(x.dtype, True)
     device = x.device
@@ -98,6 +111,10 @@ def wqbmm_mxfp4_dequantize(codes, scales, dtype, y=None, stream=None):
     """codes [M][K/2], scales [M][K/32] -> y [M][K] of `dtype`; y may be given
     (rows any multiple of 8 values apart)."""
     torch = _torch or _load()
+    if y is None and stream is None:
+        out = _calls.dequantize(codes, scales, _dtype_code(dtype, True))
+        if out is not None:
+            return out
     if not codes.is_cuda:
         raise ValueError("codes must be a device tensor")
     if codes.dim() != 2:
@@ -165,11 +182,15 @@ def wqbmm_mxfp4_matmul(x, w_tiled, N: int, activations: str = "16bit", y=None, s
     bfloat16, sums in fp32.  activations "16bit": x as it is; "mxfp4": x is
     quantised (as wqbmm_mxfp4_quantize does) in the call."""
     _torch or _load()
-    M, K, ld = _rows(x, "x")
-    code = _dtype_code(x.dtype, False)
     act = _ACTS.get(activations)
     if act is None:
         raise ValueError(f'activations must be "16bit" or "mxfp4", not {activations!r}')
+    if y is None and stream is None:
+        out = _calls.matmul(x, w_tiled, N, act)
+        if out is not None:
+            return out
+    M, K, ld = _rows(x, "x")
+    code = _dtype_code(x.dtype, False)
     device = x.device
     _check_tiled(w_tiled, K, N, "w_tiled", device)
     if y is not None:
@@ -195,6 +216,10 @@ def wqbmm_mxfp4_moe(x, router, gate_up, down, intermediate: int, top_k: int, ren
     to the lowest index), their softmax probabilities (divided by their sum if
     renormalize), and the weighted sum of down . (silu(gate . x) * (up . x))."""
     torch = _torch or _load()
+    if y is None and stream is None:
+        out = _calls.moe(x, router, gate_up, down, intermediate, top_k, renormalize)
+        if out is not None:
+            return out
     T, H, ld = _rows(x, "x")
     code = _dtype_code(x.dtype, False)
     device = x.device

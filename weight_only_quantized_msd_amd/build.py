@@ -1,4 +1,5 @@
-"""Build step for the HIP library ``libwqbmm.so`` (gfx950 only).
+"""Build step for the HIP library ``libwqbmm.so`` (gfx950 only) and the Python
+module ``_mx_calls.so`` that passes torch tensors to its MXFP4 calls.
 
 Every source is compiled with hipcc for --offload-arch=gfx950 with
 -ffp-contract=off (the MSD expansion must be rounded exactly as written; the
@@ -15,6 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(_HERE, "csrc")
 BUILD_DIR = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_HERE, "libwqbmm.so")
+CALLS_PATH = os.path.join(_HERE, "_mx_calls.so")
 SOURCES = ["msd_api.cpp", "msd_prepack.hip", "msd_prepass.hip", "msd_prefill.hip", "msd_prefill64.hip",
            "msd_decode.hip", "msd_decode_gemv.hip", "msd_probe.hip",
            "mx_api.cpp", "mx_quant.hip", "mx_gemv.hip", "mx_gemm16.hip", "mx_gemm4.hip", "mx_moe.hip"]
@@ -65,6 +67,26 @@ def build(verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def build_calls(verbose: bool = False) -> str:
+    """_mx_calls.so: the Python module of csrc/mx_torch.cpp (host code, linked to
+    torch and to libwqbmm.so beside it, which build() must have made)."""
+    import sysconfig
+    from torch.utils.cpp_extension import include_paths, library_paths
+    dirs = include_paths() + [os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+                              sysconfig.get_paths()["include"]]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM"]
+           + [a for d in dirs for a in ("-isystem", d)] + [os.path.join(CSRC, "mx_torch.cpp"), "-o", CALLS_PATH + ".tmp"]
+           + [f"-L{_HERE}", "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
+           + [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on mx_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS_PATH + ".tmp", CALLS_PATH)
+    return CALLS_PATH
+
+
 def build_host_sanitized(verbose: bool = False) -> str:
     """libwqbmm_san.so: the library with its host code (HOST_SOURCES: argument
     validation, dispatch, workspace bookkeeping) built with AddressSanitizer
@@ -99,3 +121,4 @@ def build_host_sanitized(verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_calls(verbose=True))
