@@ -14,6 +14,7 @@ namespace wqbmm {
 
 typedef float mx_f4 __attribute__((ext_vector_type(4)));
 typedef float mx_f2 __attribute__((ext_vector_type(2)));
+typedef uint32_t mx_u4 __attribute__((ext_vector_type(4)));
 typedef int mx_i4 __attribute__((ext_vector_type(4)));
 typedef int mx_i8v __attribute__((ext_vector_type(8)));
 typedef __bf16 mx_bf2 __attribute__((ext_vector_type(2)));

@@ -50,23 +50,30 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
   }
 }
 
+// A thread stores 16 bytes, so that a wave's stores are 1 KB in a row, past the
+// caches: 4099 x 11008 in fp32 took 44.6 us with ordinary stores and takes 29.2
+// (7.0 TB/s), and the inputs that follow find more of the cache (quantised and
+// read back in turn 78.4 -> 63.8 us).  Stores past the caches of 16 bytes in every
+// 32 took 67.
 template <int DT>
-__global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ codes,
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(const void* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, uint32_t kc,
                                                             int64_t chunks, void* __restrict__ y, int64_t ldy) {
+  constexpr int VALUES = DT == MX_F32 ? 4 : 8;
   for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < chunks; t += (int64_t)gridDim.x * 256) {
     const int64_t m = chunks <= 0x7fffffff ? (int64_t)((uint32_t)t / kc) : t / kc;
-    const int64_t at = m * ldy + (t - m * kc) * 8;
-    const uint32_t c = codes[t];
-    const float s = mx_scale(scales[t >> 2]);
+    const int64_t at = m * ldy + (t - m * kc) * VALUES;
+    const float s = mx_scale(scales[t / (kMxBlock / VALUES)]);
     if constexpr (DT == MX_F32) {
+      const uint32_t c = static_cast<const uint16_t*>(codes)[t];
       const mx_f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-      const mx_f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
       mx_f4* p = reinterpret_cast<mx_f4*>(static_cast<float*>(y) + at);
-      p[0] = mx_f4{a[0], a[1], b[0], b[1]};
-      p[1] = mx_f4{d[0], d[1], e[0], e[1]};
+      const mx_f4 v = {a[0], a[1], b[0], b[1]};
+      __builtin_nontemporal_store(v, p);
     } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = mx_decode8<DT>(c, s);
+      mx_u4* p = reinterpret_cast<mx_u4*>(static_cast<uint16_t*>(y) + at);
+      const mx_u4 v = __builtin_bit_cast(mx_u4, mx_decode8<DT>(static_cast<const uint32_t*>(codes)[t], s));
+      __builtin_nontemporal_store(v, p);
     }
   }
 }
@@ -130,9 +137,9 @@ hipError_t launch_mx_quantize(const void* x, int dtype, int64_t M, int64_t K, in
 
 hipError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, void* y,
                                 int dtype, int64_t ldy, hipStream_t stream) {
-  const uint32_t kc = (uint32_t)(K / 8);
+  const uint32_t kc = (uint32_t)(dtype == MX_F32 ? K / 4 : K / 8);
   const int64_t chunks = M * kc;
-  auto* c = static_cast<const uint32_t*>(codes);
+  auto* c = codes;
   auto* s = static_cast<const uint8_t*>(scales);
   auto* kernel = dtype == MX_F16 ? mx_dequantize_kernel<MX_F16>
                : dtype == MX_BF16 ? mx_dequantize_kernel<MX_BF16> : mx_dequantize_kernel<MX_F32>;

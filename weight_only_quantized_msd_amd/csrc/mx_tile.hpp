@@ -107,6 +107,8 @@ __device__ __forceinline__ void mx_store_tile(uint16_t* __restrict__ y, float* _
 // stores 16 bytes a lane, whole rows of 32*TN bytes.  `mine` (aligned to 16):
 // mx_stage_bytes<TN>() of LDS of this wave's own, half its rows at a time; rows lie
 // 16 bytes further apart than they are long, which spreads them over the banks.
+// The stores go past the caches, so that less is left to write back when the
+// kernel ends (2048 x 4096 x 4096: 51.9 -> 50.8 us with 16-bit x, 25.3 -> 24.2 with MXFP4).
 template <int TN>
 constexpr int mx_row_bytes() { return TN * 32 + 16; }
 template <int TM, int TN>
@@ -129,10 +131,10 @@ __device__ __forceinline__ void mx_store_rows(uint16_t* __restrict__ y, int M, i
 #pragma unroll
     for (int i = 0; i < H * 16 * CHUNKS / 64; ++i) {
       const int id = i * 64 + lane, row = id / CHUNKS, chunk = id % CHUNKS;
-      const uint4 v = *reinterpret_cast<const uint4*>(mine + row * mx_row_bytes<TN>() + chunk * 16);
+      const mx_u4 v = *reinterpret_cast<const mx_u4*>(mine + row * mx_row_bytes<TN>() + chunk * 16);
       const int m = m0 + half * H * 16 + row;
       const int64_t n = n0 + chunk * 8;
-      if (m < M && n < N) *reinterpret_cast<uint4*>(y + m * N + n) = v;
+      if (m < M && n < N) __builtin_nontemporal_store(v, reinterpret_cast<mx_u4*>(y + m * N + n));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
