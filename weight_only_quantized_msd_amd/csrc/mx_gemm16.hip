@@ -157,8 +157,10 @@ __device__ __forceinline__ void gemm16_loop(const uint16_t* __restrict__ x, int6
     if (i % RS == 0 && i / RS < TM) xs[i / RS] = read_x(s, j, i / RS);
     convert(j, ws, i * 4 * TN / (TM * TN), (i + 1) * 4 * TN / (TM * TN));
   };
-  // K-tile kt's stage is s, the next one's `next`.
-  auto tile = [&](auto mask_c, int kt, uint8_t* s, const uint8_t* next) __attribute__((always_inline)) {
+  // K-tile kt's stage is s, the next one's `next`.  BEFORE, SCALES: whether the
+  // last K-tile and this one load scales (the waits count these loads, and ones
+  // without a use would be taken out: the last two K-tiles load none).
+  auto tile = [&](auto mask_c, auto before_c, auto scales_c, int kt, uint8_t* s, const uint8_t* next) __attribute__((always_inline)) {
     ready(mask_c, kt, x0);
     multiply(x0, w0, [&](int i) __attribute__((always_inline)) { prepare(s, 1, x1, w1, i); });
     ready(mask_c, kt, x1);
@@ -166,12 +168,12 @@ __device__ __forceinline__ void gemm16_loop(const uint16_t* __restrict__ x, int6
     ready(mask_c, kt, x0);
     multiply(x0, w0, [&](int i) __attribute__((always_inline)) { prepare(s, 3, x1, w1, i); });
     __builtin_amdgcn_sched_barrier(0);
-    mx_wait_vm_lds<TN + G::P>();                            // the last tile's scale loads and copies stay in flight
+    mx_wait_vm_lds<(decltype(before_c)::value ? TN : 0) + G::P>();   // what the last K-tile issued stays in flight
     mx_barrier();
     ready(mask_c, kt, x1);
 #pragma unroll
     for (int c = 0; c < TN; ++c) f[c] = mx_scale((sc[c] >> (8 * ((kt + 1) & 3))) & 0xffu);
-    load_scales(within(kt + 2), sc);
+    if constexpr (decltype(scales_c)::value) load_scales(within(kt + 2), sc);
     const int k3 = within(kt + 3);
     constexpr int PRODUCTS = TM * TN, AT_ONCE = (G::P + PRODUCTS - 1) / PRODUCTS, CS = PRODUCTS * AT_ONCE / G::P;
     multiply(x1, w1, [&](int i) __attribute__((always_inline)) {
@@ -206,16 +208,18 @@ __device__ __forceinline__ void gemm16_loop(const uint16_t* __restrict__ x, int6
     raw[c] = read_w(s0, c);
     w0[c] = mx_decode8<G::CT>(raw[c].x, f[c]);
   }
+  using Yes = std::true_type;
+  using No = std::false_type;
   const int whole = min(kt_hi, blocks / 4);                 // K-tiles that end within K
   int kt = kt_lo;
   for (; kt + 3 <= whole; kt += 3) {
-    tile(std::false_type{}, kt, s0, s1);
-    tile(std::false_type{}, kt + 1, s1, s2);
-    tile(std::false_type{}, kt + 2, s2, s0);
+    tile(No{}, Yes{}, Yes{}, kt, s0, s1);
+    tile(No{}, Yes{}, Yes{}, kt + 1, s1, s2);
+    tile(No{}, Yes{}, Yes{}, kt + 2, s2, s0);
   }
-  if (kt < kt_hi) tile(std::true_type{}, kt, s0, s1);
-  if (kt + 1 < kt_hi) tile(std::true_type{}, kt + 1, s1, s2);
-  if (kt + 2 < kt_hi) tile(std::true_type{}, kt + 2, s2, s0);
+  if (kt < kt_hi) tile(Yes{}, Yes{}, Yes{}, kt, s0, s1);
+  if (kt + 1 < kt_hi) tile(Yes{}, Yes{}, No{}, kt + 1, s1, s2);
+  if (kt + 2 < kt_hi) tile(Yes{}, No{}, No{}, kt + 2, s2, s0);
   mx_wait_vm_lds<0>();                                      // copies must not outlive the workgroup's LDS
   mx_wait_results();
 }
@@ -338,7 +342,7 @@ MxGemmPlan mx_choose(const MxTileCost* tiles, int count, double base, int64_t M,
 
 // Measured at 2048 x 4096 x 4096 (M, K, N): 52 us with the first tile, 62 with
 // the others; at 512 rows 30, 27 and 19 us; at 130 x 4128 x 4099 24, 18 and 17.
-constexpr MxTileCost kTiles[] = {{128, 256, 6.0, 1.30}, {64, 256, 2.0, 0.85}, {64, 128, 0.0, 0.45}};
+constexpr MxTileCost kTiles[] = {{128, 256, 6.0, 1.30}, {64, 256, 1.0, 0.83}, {64, 128, 0.0, 0.45}};
 
 MxGemmPlan mx_gemm16_plan(int64_t M, int64_t K, int64_t N) { return mx_choose(kTiles, 3, 4.0, M, K, N); }
 

@@ -147,22 +147,25 @@ __device__ __forceinline__ void gemm4_tile(const MxTiled& x, const MxTiled& w, i
   // stand between them, in this order (the compiler moves no memory access
   // across a volatile asm).  The reads are issued in the first three quarters
   // of the phase, so that the wait for them at its end finds them done.
-  auto multiply = [&](auto ic, const uint4 (&o)[S], const uint8_t* next, uint4 (&o_next)[S], int kt, uint8_t* into,
-                      int q_next) __attribute__((always_inline)) {
+  auto multiply = [&](auto ic, auto scales_c, const uint4 (&o)[S], const uint8_t* next, uint4 (&o_next)[S], int kt,
+                      uint8_t* into, int q_next) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
+    constexpr bool SCALES = decltype(scales_c)::value;
     constexpr int RS = TM * TN * 3 / 4 / S, CS = TM * TN / P, SS = TM * TN / S;   // products from one to the next
     const int k = offset_of(kt);
 #pragma unroll
     for (int at = 0; at < TM * TN; ++at) {
       const int c = at / TM, t = at % TM;
       if (at % RS == 0 && at / RS < S) read(next, o_next, at / RS);
-      if (i == 0 && at % SS == 0 && at / SS < S) load_scale(at / SS, q_next, nx, nw);
+      if (SCALES && at % SS == 0 && at / SS < S) load_scale(at / SS, q_next, nx, nw);
       mfma4_into<i>(acc[c][t], o[TM + c], scw[c], o[t], scx[t]);
       if (at % CS == 1 && at / CS < P) copy(at / CS, k, into);
     }
   };
   // The wait for the copies leaves later ones in flight; in phase 1 these are
-  // phase 0's, whose scale loads are among them.
+  // phase 0's, whose scale loads are among them.  After the last whole quad no
+  // scales follow: phase 0 then loads none (loads without a use would be taken
+  // out, and phase 1 would count on them), and phase 1 waits like the others.
   auto meet = [&](auto nc) __attribute__((always_inline)) {
     mx_wait_vm_lds<decltype(nc)::value>();
     mx_barrier();
@@ -172,22 +175,22 @@ __device__ __forceinline__ void gemm4_tile(const MxTiled& x, const MxTiled& w, i
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;
   using WaitP = std::integral_constant<int, P>;
-  using WaitPS = std::integral_constant<int, P + S>;
-  auto phase0 = [&](int q) __attribute__((always_inline)) {
+  using None = std::false_type;
+  auto phase0 = [&](auto scales_c, int q) __attribute__((always_inline)) {
     meet(WaitP{});
-    multiply(I0{}, o0, s1, o1, 4 * q + 3, s3, q + 1);
+    multiply(I0{}, scales_c, o0, s1, o1, 4 * q + 3, s3, q + 1);
   };
-  auto phase1 = [&](int q) __attribute__((always_inline)) {
-    meet(WaitPS{});
-    multiply(I1{}, o1, s2, o0, 4 * q + 4, s0, 0);
+  auto phase1 = [&](auto scales_c, int q) __attribute__((always_inline)) {
+    meet(std::integral_constant<int, decltype(scales_c)::value ? P + S : P>{});
+    multiply(I1{}, None{}, o1, s2, o0, 4 * q + 4, s0, 0);
   };
   auto phase2 = [&](int q) __attribute__((always_inline)) {
     meet(WaitP{});
-    multiply(I2{}, o0, s3, o1, 4 * q + 5, s1, 0);
+    multiply(I2{}, None{}, o0, s3, o1, 4 * q + 5, s1, 0);
   };
   auto phase3 = [&](int q) __attribute__((always_inline)) {
     meet(WaitP{});
-    multiply(I3{}, o1, s0, o0, 4 * q + 6, s2, 0);
+    multiply(I3{}, None{}, o1, s0, o0, 4 * q + 6, s2, 0);
   };
 
 #pragma unroll
@@ -201,8 +204,8 @@ __device__ __forceinline__ void gemm4_tile(const MxTiled& x, const MxTiled& w, i
   const int whole = min(q_hi, w.kt / 4);
   int q = q_lo;
   for (; q < whole; ++q) {
-    phase0(q);
-    phase1(q);
+    phase0(std::true_type{}, q);
+    phase1(std::true_type{}, q);
     phase2(q);
     phase3(q);
 #pragma unroll
@@ -211,8 +214,8 @@ __device__ __forceinline__ void gemm4_tile(const MxTiled& x, const MxTiled& w, i
     for (int c = 0; c < TN; ++c) scw[c] = nw[c];
   }
   if (q < q_hi) {                                           // the last quad ends early
-    phase0(q);
-    if (4 * q + 1 < w.kt) phase1(q);
+    phase0(None{}, q);
+    if (4 * q + 1 < w.kt) phase1(None{}, q);
     if (4 * q + 2 < w.kt) phase2(q);
   }
   mx_wait_vm<0>();                                          // copies must not outlive the workgroup's LDS
