@@ -117,6 +117,8 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(const uint8_t* __restrict_
   if (any) atomicOr(&wide, 1);
   __syncthreads();
   if (threadIdx.x == 0) out_flags[p] = wide ? 0u : kMxFlagF16;
+  // the flags fill whole 16 bytes: equal weights are equal in every byte
+  if (p == gridDim.x - 1 && threadIdx.x < 3 && (p + 1 + threadIdx.x) / 4 == p / 4) out_flags[p + 1 + threadIdx.x] = 0;
 }
 
 // A thread per chunk; past 2^22 workgroups the threads loop (a grid holds fewer than 2^32 threads).
