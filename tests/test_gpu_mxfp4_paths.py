@@ -251,3 +251,19 @@ def test_graph_replays_of_the_other_paths(torch):
             graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, outs)), i
+
+
+def test_example(torch, capsys):
+    """The example's block: the kernels add a rounding, quantising what MXFP4 costs."""
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mxfp4_block.py")
+    spec = importlib.util.spec_from_file_location("mxfp4_block", at)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    report, y, ids, weights = module.main(["--hidden", "256", "--ffn", "352", "--prompt", "70"])
+    for name, (cost, added) in report.items():
+        # a uniform rounding of at most 2^-8 of the value; each factor in MXFP4 is off by at most a quarter of its value
+        assert added <= 2.0 ** -8 and cost <= 0.25 * (2 + 0.25), name
+    assert torch.isfinite(y).all() and (weights.sum(1) - 1).abs().max() <= 16 * 2.0 ** -24
+    assert "decoding step" in capsys.readouterr().out
