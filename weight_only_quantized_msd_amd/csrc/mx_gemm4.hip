@@ -11,42 +11,47 @@
 
 namespace wqbmm {
 
-// x -> tiled MXFP4.  A wave takes a panel's quad of K-tiles; a lane holds whole
+// x -> tiled MXFP4.  A wave takes two of a panel's K-tiles; a lane holds whole
 // blocks, so nothing crosses lanes.
+constexpr int PREP_TILES = 2;
 template <int DT>
 __global__ __launch_bounds__(256) void mx_prep_kernel(const uint16_t* __restrict__ x, int64_t ldx, int M, int blocks,
                                                       int kt, int kq, int64_t waves, uint8_t* __restrict__ codes,
-                                                      uint32_t* __restrict__ scales) {
+                                                      uint16_t* __restrict__ scales) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= waves) return;
-  const int64_t p = id / kq;
-  const int q = (int)(id % kq);
+  const int per = kq * 4 / PREP_TILES;
+  const int64_t p = id / per;
+  const int t0 = (int)(id % per) * PREP_TILES;
   const int64_t m = p * kMxPanel + r;
-  uint4 v[4][4] = {};
+  uint4 v[PREP_TILES][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = 4 * (4 * q + i) + g;
-    if (m < M && b < blocks) {
+  for (int i = 0; i < PREP_TILES; ++i) {
+    const int b = 4 * (t0 + i) + g;
+    const bool in = m < M && b < blocks;
+    const uint4* const from = reinterpret_cast<const uint4*>(x + min(m, (int64_t)M - 1) * ldx + (in ? (int64_t)b * kMxBlock : 0));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[i][j] = reinterpret_cast<const uint4*>(x + m * ldx + (int64_t)b * kMxBlock)[j];
+    for (int j = 0; j < 4; ++j) v[i][j] = from[j];
+    if (!in) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  uint32_t dword = 0;
+  uint32_t both = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (4 * q + i >= kt) break;
+  for (int i = 0; i < PREP_TILES; ++i) {
+    if (t0 + i >= kt) break;
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = mx_max16(v[i][j], top);
     const uint32_t s = mx_scale_byte(mx_top_bits<DT>(mx_max16_fold(top)));
     const float f = mx_scale(s);
-    dword |= s << (8 * i);
-    *reinterpret_cast<uint4*>(codes + ((p * kt + 4 * q + i) * 64 + lane) * 16) = make_uint4(
+    both |= s << (8 * i);
+    *reinterpret_cast<uint4*>(codes + ((p * kt + t0 + i) * 64 + lane) * 16) = make_uint4(
         mx_encode8<DT>(v[i][0], f), mx_encode8<DT>(v[i][1], f), mx_encode8<DT>(v[i][2], f), mx_encode8<DT>(v[i][3], f));
   }
-  scales[(p * kq + q) * 64 + lane] = dword;
+  scales[((p * kq + t0 / 4) * 64 + lane) * 2 + (t0 / 2 & 1)] = (uint16_t)both;
 }
 
 // c += a . b in place (mx_tile.hpp).  SEL: the scale byte of both operands.
@@ -272,9 +277,9 @@ static hipError_t gemm4_dt(const void* x, int64_t ldx, const MxTiled& w, int64_t
   auto* yp = static_cast<uint16_t*>(y);
   const MxTiled xt = mx_view(ws, K, M);
   auto* codes = ws;
-  auto* scales = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(xt.scales));
+  auto* scales = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(xt.scales));
   float* part = sp > 1 ? reinterpret_cast<float*>(ws + plan.x_bytes) : nullptr;
-  const int64_t waves = (int64_t)xt.panels * xt.kq;
+  const int64_t waves = (int64_t)xt.panels * xt.kq * 4 / PREP_TILES;
   hipError_t e = mx_launch(mx_prep_kernel<DT>, dim3((unsigned)((waves + 3) / 4)), dim3(256), stream, xp, ldx, m, blocks,
                            xt.kt, xt.kq, waves, codes, scales);
   if (e != hipSuccess) return e;
