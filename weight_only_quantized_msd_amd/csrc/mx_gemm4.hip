@@ -2,7 +2,7 @@
 // rows: a preparation kernel quantises x into the tiled layout, and the product
 // runs on v_mfma_scale_f32_16x16x128_f8f6f4, both operands as they lie.
 //
-// 2001 x 8192 x 28672 (M, K, N): 225 us and 11 us of preparation, 4.2 PFLOP/s.
+// 2001 x 8192 x 28672 (M, K, N): 212-220 us and 8.8 of preparation, 4.3 PFLOP/s.
 // The matrix cores alone, on random operands in registers, reached 6.8 (the
 // card's power limit; 9.6 on zeros); with the barriers and waits 6.1, with the LDS
 // reads 5.3, with the copies 4.6 at long K; the rest are the first copies and the

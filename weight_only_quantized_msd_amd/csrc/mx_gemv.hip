@@ -17,7 +17,7 @@
 // into two exact bf16 parts, at twice the MFMAs.
 //
 // Bound by the weights' bytes and one trip to memory: 1 x 4096 x 4096 (M, K, N)
-// 3.4 us, 16 x 4096 x 11008 7.8 us (24 MB), 16 x 8192 x 28672 31 us (125 MB, 4.0 TB/s).
+// 3.4-3.8 us, 16 x 4096 x 11008 7.7 us (24 MB), 16 x 8192 x 28672 31 us (125 MB, 4.0 TB/s).
 #include <algorithm>
 
 #include "mx_tile.hpp"

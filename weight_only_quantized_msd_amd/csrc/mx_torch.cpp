@@ -4,7 +4,7 @@
 // Many of these calls run in a few microseconds, and in Python the checks, the
 // outputs' allocation (1.5 us each) and ctypes took longer than that: 8.1 us to
 // issue a quantisation and 7.3 a product, of which the launch itself takes 2.9;
-// this way 4.9 and 4.4.  Each function takes the ordinary case, outputs allocated
+// this way 4.8 and 3.9.  Each function takes the ordinary case, outputs allocated
 // for the current stream of the current device, and returns None for anything
 // else, a call that the library refuses among them: the wrappers of _mxfp4.py
 // then take the long way, which says what is wrong.
