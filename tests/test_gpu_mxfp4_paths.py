@@ -171,6 +171,32 @@ def test_moe_a_nan_weight_stays_with_its_expert(torch, T, H, inter, E, k):
             assert same(torch, y[hit][:, rest].contiguous(), clean[hit][:, rest].contiguous())
 
 
+@pytest.mark.parametrize("values", ["few", "special", "equal"])
+@pytest.mark.parametrize("E,k", [(1, 1), (7, 7), (32, 16), (33, 5), (64, 16), (65, 1), (65, 16), (128, 8), (200, 16), (256, 16)])
+@pytest.mark.parametrize("T", [1, 2])
+def test_moe_choices(torch, T, E, k, values):
+    """Larger logits first, NaN above all, -0 equal to +0, equal logits by index; the logits are exact."""
+    import weight_only_quantized_msd_amd as W
+    rng = np.random.default_rng(E + k)
+    H, inter = 64, 32
+    of = {"few": [-1.0, -0.0, 0.0, 0.5, 3.0], "special": [-np.inf, -2.0, -0.0, 0.0, 1.0, np.inf, np.nan], "equal": [-1.5]}
+    logits = rng.choice(of[values], E)
+    x, router = np.zeros((T, H)), np.zeros((E, H))
+    x[:, 0], router[:, 0] = 1.0, logits
+    x, router = on_gpu(torch, x, "bf16")[0], on_gpu(torch, router, "bf16")[0]
+    gt, dn = tiled(torch, *random_weights(rng, (E, 2 * inter, H))), tiled(torch, *random_weights(rng, (E, H, inter)))
+    key = np.where(np.isnan(logits), np.inf, np.clip(logits, -1e9, 1e9))
+    order = np.argsort(-key, kind="stable")[:k]
+    for renorm in (True, False):
+        _, ids, weights = W.wqbmm_mxfp4_moe(x, router, gt, dn, inter, k, renormalize=renorm)
+        assert np.array_equal(ids.cpu().numpy(), np.tile(order, (T, 1)))
+        if np.isfinite(logits).all():
+            p = np.exp(logits - logits.max())
+            p = p[order] / (p[order].sum() if renorm else p.sum())
+            # exp and its argument, the division, a sum of E terms: fp32 steps
+            assert (np.abs(weights.double().cpu().numpy() - p) <= (E + 16) * 2.0 ** -24 * p).all()
+
+
 def test_moe_one_token_ties_and_nan(torch):
     import weight_only_quantized_msd_amd as W
     T, H, inter, E, k = 1, 64, 32, 90, 4

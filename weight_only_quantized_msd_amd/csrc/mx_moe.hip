@@ -84,46 +84,102 @@ __device__ __forceinline__ void router_logits(const uint4* __restrict__ xr, cons
   for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
 }
 
-// The choices of one token, from its logits, by all `waves` of a workgroup: an
-// expert's rank is the number of experts ahead of it (larger logit, then lower
-// index); ranks below k are the choices, and lane j of every wave gets the j-th
-// one's index and softmax weight.
-struct Choice {
-  float logits[kMoeMaxE];
-  uint32_t keys[kMoeMaxE];
-  int rank[kMoeMaxE], chosen[kMoeMaxK];
+// The choices of one token, by one wave: lane l holds the logits f[r] of experts
+// 64 * r + l.  Lane j < k gets the j-th choice (larger logit first, then lower
+// index), and `mine / wave_sum(sum)` is its softmax weight.
+struct Choice {                                 // of the wave's own, in LDS
+  int id[kMoeMaxK];
+  float logit[kMoeMaxK];
 };
-__device__ __forceinline__ void choose(Choice& c, int E, int k, bool renormalize, int tid, int threads, int& my_id,
-                                       float& my_weight) {
-  const int lane = tid & 63, wave = tid >> 6, waves = threads >> 6;
-  for (int e = tid; e < E; e += threads) {
-    c.keys[e] = order_key(c.logits[e]);
-    c.rank[e] = 0;
+
+// How many of the first n lanes are ahead of each lane.
+__device__ __forceinline__ int lanes_ahead(uint32_t key, int n, int lane) {
+  int ahead = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key, j);
+    ahead += other > key || (other == key && j < lane);
   }
-  __syncthreads();
-  const int part = (E + waves - 1) / waves, lo = wave * part, hi = min(E, lo + part);
-  for (int e = lane; e < E; e += 64) {
-    const uint32_t mine = c.keys[e];
-    int ahead = 0;
-    for (int o = lo; o < hi; ++o) {
-      const uint32_t other = c.keys[o];
-      ahead += other > mine || (other == mine && o < e);
+  return ahead;
+}
+
+// Up to 32 experts are ranked as they are.  Of more, the k-th largest key is
+// found bit by bit (a comparison and a count of lanes each); the experts above
+// it, and as many of those equal to it as there is room for, lowest index first,
+// are ranked.  (One token, us of the layer: H = 4096, I = 1024, 256 experts, 8
+// chosen 35 ranked by all waves of a workgroup, 21 this way; 2048, 1024, 64, 8
+// 16.9 ranked, 15.2 this way; 512, 256, 4, 1 10.0 this way, 9.0 ranked.)
+template <int R, bool RANK>
+__device__ __forceinline__ void choose_from(const float (&f)[R], Choice& c, int E, int k, bool renormalize, int lane,
+                                            int& my_id, float& mine, float& sum) {
+  uint32_t key[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) key[r] = 64 * r + lane < E ? order_key(f[r]) : 0u;    // no float has key 0
+  int rank;
+  float my_logit;
+  if constexpr (RANK) {
+    rank = lanes_ahead(key[0], E, lane);
+    my_id = lane;
+    my_logit = f[0];
+  } else {
+    uint32_t kth = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t at = kth | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) n += __popcll(__ballot(key[r] >= at));
+      if (n >= k) kth = at;
     }
-    if (ahead) atomicAdd(&c.rank[e], ahead);
+    int room = k, n = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) room -= __popcll(__ballot(key[r] > kth));
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t same = __ballot(key[r] == kth);
+      const bool in = key[r] > kth || (key[r] == kth && __popcll(same & below) < room);
+      room -= min(room, __popcll(same));
+      const uint64_t all = __ballot(in);
+      if (in) {
+        c.id[n + __popcll(all & below)] = 64 * r + lane;
+        c.logit[n + __popcll(all & below)] = f[r];
+      }
+      n += __popcll(all);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    my_id = c.id[min(lane, k - 1)];
+    my_logit = c.logit[min(lane, k - 1)];
+    rank = lanes_ahead(order_key(my_logit), k, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  __syncthreads();
-  for (int e = tid; e < E; e += threads)
-    if (c.rank[e] < k) c.chosen[c.rank[e]] = e;
-  __syncthreads();
-  my_id = lane < k ? c.chosen[lane] : 0;
-  const float top = c.logits[c.chosen[0]];
-  const float mine = lane < k ? expf(c.logits[my_id] - top) : 0.0f;
-  float sum = mine;
+  if (lane < (RANK ? E : k) && rank < k) {
+    c.id[rank] = my_id;
+    c.logit[rank] = my_logit;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  my_id = lane < k ? c.id[lane] : 0;
+  const float top = c.logit[0];
+  mine = lane < k ? expf(c.logit[lane] - top) : 0.0f;
+  sum = mine;
   if (!renormalize) {                           // over all experts instead
     sum = 0.0f;
-    for (int e = lane; e < E; e += 64) sum += expf(c.logits[e] - top);
+#pragma unroll
+    for (int r = 0; r < R; ++r) sum += 64 * r + lane < E ? expf(f[r] - top) : 0.0f;
   }
-  my_weight = mine / wave_sum(sum);
+}
+__device__ __forceinline__ void choose(const float* logits, Choice& c, int E, int k, bool renormalize, int lane,
+                                       int& my_id, float& mine, float& sum) {
+  auto from = [&](auto rc, auto rank) __attribute__((always_inline)) {
+    constexpr int R = decltype(rc)::value;
+    float f[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) f[r] = logits[min(64 * r + lane, E - 1)];
+    choose_from<R, decltype(rank)::value>(f, c, E, k, renormalize, lane, my_id, mine, sum);
+  };
+  if (E <= 32) from(std::integral_constant<int, 1>{}, std::true_type{});
+  else if (E <= 64) from(std::integral_constant<int, 1>{}, std::false_type{});
+  else from(std::integral_constant<int, kMoeMaxE / 64>{}, std::false_type{});
 }
 
 // One workgroup per token, four experts a wave at a time.
@@ -133,9 +189,10 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64) void mx_route_kernel(const uint16
                                                                     int E, int k, int renormalize,
                                                                     int32_t* __restrict__ ids,
                                                                     float* __restrict__ weights) {
+  __shared__ float logits[kMoeMaxE];
   __shared__ Choice c;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
   constexpr int N = 4;
   for (int e0 = wave * N; e0 < E; e0 += ROUTE_WAVES * N) {
@@ -143,15 +200,17 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64) void mx_route_kernel(const uint16
     router_logits<DT, N>(reinterpret_cast<const uint4*>(x + t * ldx), router, H, E, e0, lane, s);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (lane == 0 && e0 + i < E) c.logits[e0 + i] = s[i];
+      if (lane == 0 && e0 + i < E) logits[e0 + i] = s[i];
   }
   __syncthreads();
+  if (wave != 0) return;
   int id;
-  float weight;
-  choose(c, E, k, renormalize != 0, tid, ROUTE_WAVES * 64, id, weight);
-  if (wave == 0 && lane < k) {
+  float mine, sum;
+  choose(logits, c, E, k, renormalize != 0, lane, id, mine, sum);
+  sum = wave_sum(sum);
+  if (lane < k) {
     ids[t * k + lane] = id;
-    weights[t * k + lane] = weight;
+    weights[t * k + lane] = mine / sum;
   }
 }
 
@@ -208,6 +267,14 @@ __device__ __forceinline__ void store_h(uint16_t* __restrict__ hi, uint16_t* __r
   }
   *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
   *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
+}
+
+// share * silu(a) * b
+__device__ __forceinline__ mx_f4 gated(mx_f4 a, mx_f4 b, float share) {
+  mx_f4 h;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = a[j] / (1.0f + expf(-a[j])) * b[j] * share;
+  return h;
 }
 
 // h's rows, one for each pair, hold whole K-tiles (what lies past I is not used).
@@ -356,11 +423,7 @@ __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& 
     const int at = (blockIdx.x * Q + qm / MT) * kMxPanel + 4 * (lane >> 4);
     if (i >= rows || at >= I) continue;
     const mx_f4 a = total<P, MT>(part, qm, UP_WAVES, lane), b = total<P, MT>(part, Q * MT + qm, UP_WAVES, lane);
-    const float share = share_of(i);
-    mx_f4 h;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = a[j] / (1.0f + expf(-a[j])) * b[j] * share;
-    store_h(h_hi, h_lo, pair_of(i) * h_pitch(I) + h_place(at), h);
+    store_h(h_hi, h_lo, pair_of(i) * h_pitch(I) + h_place(at), gated(a, b, share_of(i)));
   }
 }
 
@@ -467,6 +530,7 @@ __global__ __launch_bounds__(256) void mx_moe_sum_kernel(const float* __restrict
 // one reads the router at some 100 GB/s), each workgroup of the gate and up
 // product then chooses by itself, and one workgroup adds all experts' shares of
 // its columns of y.
+constexpr int ONE_UP_WAVES = 4, ONE_DOWN_WAVES = 16;
 template <int DT>
 __global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __restrict__ x,
                                                             const uint16_t* __restrict__ router, int H, int E,
@@ -478,93 +542,160 @@ __global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __re
   if (lane == 0 && e < E) logits[e] = s[0];
 }
 
-template <int DT>
-__global__ __launch_bounds__(UP_WAVES * 64) void mx_one_up_kernel(const uint16_t* __restrict__ x, MxTiled w,
-                                                                 const float* __restrict__ logits, int E, int k,
-                                                                 int renormalize, int blocks, int I,
-                                                                 int32_t* __restrict__ ids,
-                                                                 float* __restrict__ weights,
-                                                                 uint16_t* __restrict__ h_hi,
-                                                                 uint16_t* __restrict__ h_lo) {
-  __shared__ mx_f4 part[UP_WAVES * 2 * 64];
-  __shared__ Choice c;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < E; e += UP_WAVES * 64) c.logits[e] = logits[e];
-  __syncthreads();
-  int id;
-  float weight;
-  choose(c, E, k, renormalize != 0, tid, UP_WAVES * 64, id, weight);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0 && lane < k) {
-    ids[lane] = id;
-    weights[lane] = weight;
+// A unit of a row, 512 values from 512 * q on: 16 bytes a lane.  In h chunk
+// lane % 16 of a K-tile belongs to block lane % 4 (h_place), in x to block
+// lane % 16 / 4.
+struct OneRow {
+  uint4 hi, lo;
+};
+template <bool PAIR>
+__device__ __forceinline__ OneRow one_row(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
+                                          int64_t row, int q, int blocks, int lane) {
+  OneRow v = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (4 * (4 * q + (lane >> 4)) + (PAIR ? lane & 3 : (lane >> 2) & 3) < blocks) {
+    const int64_t at = row + (int64_t)q * 4 * kMxTile + lane * 8;
+    v.hi = *reinterpret_cast<const uint4*>(src + at);
+    if constexpr (PAIR) v.lo = *reinterpret_cast<const uint4*>(src_lo + at);
   }
-  const int slot = blockIdx.y, expert = __builtin_amdgcn_readfirstlane(__shfl(id, slot));
-  const float share = __shfl(weight, slot);
-  up_rows<DT, 1, 1>(
-      x, [](int) __attribute__((always_inline)) { return (int64_t)0; },
-      [&](int) __attribute__((always_inline)) { return slot; },
-      [&](int) __attribute__((always_inline)) { return share; }, w, expert, 1, blocks, I, wave, lane, part, h_hi, h_lo);
+  return v;
 }
 
-// Workgroup: a panel of 16 columns of y.  A unit is a choice's quad of K-tiles;
-// the next unit's codes are loaded while the present one is multiplied.
-constexpr int ONE_WAVES = 8;
-template <int DT>
-__global__ __launch_bounds__(ONE_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h_hi,
-                                                                    const uint16_t* __restrict__ h_lo, MxTiled w,
-                                                                    const int32_t* __restrict__ ids, int k, int I,
-                                                                    int H, uint16_t* __restrict__ y) {
-  __shared__ mx_f4 part[ONE_WAVES * 64];
-  const int lane = threadIdx.x & 63, g = lane >> 4, blocks = I / kMxBlock;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int units = k * w.kq;
-  mx_f4 acc[1][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}};
-  uint4 c[4], next[4];
-  uint32_t sc = 0, sc_next = 0;
-  auto load = [&](int u, uint4 (&to)[4], uint32_t& s) __attribute__((always_inline)) {
+// P panels' products with one row (x), or the sum over slots of each slot's (h).
+// A unit is a slot's quad of K-tiles, the waves take them in turn; the next
+// unit's row and codes are loaded while the present one is multiplied, and the
+// row goes by way of LDS of the wave's own (2 KB), so that all of a unit is one
+// trip to memory (1 token, 64 experts, 8 chosen, H = 2048, I = 1024: operands read
+// in place, tile by tile, the down product took 7.4 us instead of 4.5, the up
+// product 8.9 instead of 8.1).  `v` is the first unit's row.  fp16 x: two bf16
+// parts unless `exact`, i.e. all of the panels' weights are exact in fp16.
+template <int DT, bool PAIR, int P, int WAVES, typename RowAt, typename PanelAt>
+__device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
+                                          OneRow v, RowAt&& row_at, PanelAt&& panel_at, bool exact, int slots,
+                                          const MxTiled& w, int blocks, int wave, int lane, uint4* mine,
+                                          mx_f4 (&acc)[P][1]) {
+  const int g = lane >> 4, units = slots * w.kq;
+  uint4 c[P][4], next[P][4];
+  uint32_t sc[P], sc_next[P];
+  OneRow v_next = v;
+  auto load = [&](int u, uint4 (&to)[P][4], uint32_t (&s)[P]) __attribute__((always_inline)) {
     const int q = u % w.kq;
-    const int64_t panel = (int64_t)ids[u / w.kq] * (H / kMxPanel) + blockIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      to[i] = *reinterpret_cast<const uint4*>(w.codes + ((panel * w.kt + min(4 * q + i, w.kt - 1)) * 64 + lane) * 16);
-    s = *reinterpret_cast<const uint32_t*>(w.scales + ((panel * w.kq + q) * 64 + lane) * 4);
+    for (int p = 0; p < P; ++p) {
+      const int64_t panel = panel_at(u / w.kq, p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[p][i] = *reinterpret_cast<const uint4*>(w.codes + ((panel * w.kt + min(4 * q + i, w.kt - 1)) * 64 + lane) * 16);
+      s[p] = *reinterpret_cast<const uint32_t*>(w.scales + ((panel * w.kq + q) * 64 + lane) * 4);
+    }
   };
   if (wave < units) load(wave, c, sc);
-  for (int u = wave; u < units; u += ONE_WAVES) {
-    if (u + ONE_WAVES < units) load(u + ONE_WAVES, next, sc_next);
-    const int q = u % w.kq;
-    const int64_t row = u / w.kq * h_pitch(I);
-    uint4 v[4][4] = {}, l[4][4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((lane & 15) == 0 && 4 * (4 * q + i) + g < blocks) {
-        const int64_t at = row + (4 * q + i) * kMxTile + g * 8;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] = *reinterpret_cast<const uint4*>(h_hi + at + j * 32);
-          l[i][j] = *reinterpret_cast<const uint4*>(h_lo + at + j * 32);
-        }
-      }
+  for (int u = wave; u < units; u += WAVES) {
+    const int q = u % w.kq, after = u + WAVES;
+    mine[lane] = v.hi;
+    if constexpr (PAIR) mine[64 + lane] = v.lo;
+    if (after < units) {
+      v_next = one_row<PAIR>(src, src_lo, row_at(after / w.kq), after % w.kq, blocks, lane);
+      load(after, next, sc_next);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (4 * q + i >= w.kt) break;
-      const float f = mx_scale((sc >> (8 * i)) & 0xffu);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 a = mx_decode8<MX_BF16>(dword_of(c[i], j), f);
-        acc[0][0] = mx_mfma16<MX_BF16>(a, v[i][j], acc[0][0]);
-        acc[0][0] = mx_mfma16<MX_BF16>(a, l[i][j], acc[0][0]);
+        const int at = 16 * i + (PAIR ? 4 * j + g : 4 * g + j);
+        uint4 a = mine[at], b;
+        if constexpr (PAIR) b = mine[64 + at];
+        auto tile = [&](auto ct, bool two) __attribute__((always_inline)) {
+          constexpr int CT = decltype(ct)::value;
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint4 d = mx_decode8<CT>(dword_of(c[p][i], j), mx_scale((sc[p] >> (8 * i)) & 0xffu));
+            acc[p][0] = mx_mfma16<CT>(d, a, acc[p][0]);
+            if (two) acc[p][0] = mx_mfma16<CT>(d, b, acc[p][0]);
+          }
+        };
+        if constexpr (PAIR) tile(std::integral_constant<int, MX_BF16>{}, true);
+        else if (DT == MX_BF16 || exact) tile(std::integral_constant<int, DT>{}, false);
+        else {
+          const uint4 both = a;
+          mx_split8(both, a, b);
+          tile(std::integral_constant<int, MX_BF16>{}, true);
+        }
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = next[i];
-    sc = sc_next;
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[p][i] = next[p][i];
+      sc[p] = sc_next[p];
+    }
+    v = v_next;
   }
+}
+
+// Workgroup: a panel of 16 rows of I, one choice.
+template <int DT>
+__global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint16_t* __restrict__ x, MxTiled w,
+                                                                     const float* __restrict__ logits, int E, int k,
+                                                                     int renormalize, int blocks, int I,
+                                                                     int32_t* __restrict__ ids,
+                                                                     float* __restrict__ weights,
+                                                                     uint16_t* __restrict__ h_hi,
+                                                                     uint16_t* __restrict__ h_lo) {
+  __shared__ mx_f4 part[ONE_UP_WAVES * 2 * 64];
+  __shared__ uint4 rows[ONE_UP_WAVES][64];
+  __shared__ Choice choices[ONE_UP_WAVES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const OneRow first = one_row<false>(x, x, 0, wave, blocks, lane);
+  int id;
+  float mine, sum;
+  choose(logits, choices[wave], E, k, renormalize != 0, lane, id, mine, sum);
+  const int slot = blockIdx.y, expert = __builtin_amdgcn_readlane(id, slot), half = I / kMxPanel;
+  const int64_t panel = (int64_t)expert * (2 * half) + blockIdx.x;
+  const bool exact = DT == MX_BF16 || (w.flags[panel] & w.flags[panel + half] & kMxFlagF16) != 0;
+  mx_f4 acc[2][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}, {mx_f4{0.f, 0.f, 0.f, 0.f}}};
+  one_units<DT, false, 2, ONE_UP_WAVES>(
+      x, x, first, [](int) __attribute__((always_inline)) { return (int64_t)0; },
+      [&](int, int p) __attribute__((always_inline)) { return panel + p * half; }, exact, 1, w, blocks, wave, lane,
+      rows[wave], acc);
+  share_sums<2, 1>(part, acc, wave, lane);
+  if (wave != 0) return;
+  const float weight = mine / wave_sum(sum), share = __shfl(weight, slot);
+  if (blockIdx.x == 0 && slot == 0 && lane < k) {
+    ids[lane] = id;
+    weights[lane] = weight;
+  }
+  if ((lane & 15) == 0) {
+    const mx_f4 a = total<2, 1>(part, 0, ONE_UP_WAVES, lane), b = total<2, 1>(part, 1, ONE_UP_WAVES, lane);
+    store_h(h_hi, h_lo, slot * h_pitch(I) + h_place(blockIdx.x * kMxPanel + 4 * (lane >> 4)), gated(a, b, share));
+  }
+}
+
+// Workgroup: a panel of 16 columns of y, all choices.
+template <int DT>
+__global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h_hi,
+                                                                         const uint16_t* __restrict__ h_lo, MxTiled w,
+                                                                         const int32_t* __restrict__ ids, int k,
+                                                                         int I, int H, uint16_t* __restrict__ y) {
+  __shared__ mx_f4 part[ONE_DOWN_WAVES * 64];
+  __shared__ uint4 rows[ONE_DOWN_WAVES][2 * 64];
+  const int lane = threadIdx.x & 63, blocks = I / kMxBlock;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  auto row_at = [&](int slot) __attribute__((always_inline)) { return slot * h_pitch(I); };
+  const OneRow first = wave < k * w.kq ? one_row<true>(h_hi, h_lo, row_at(wave / w.kq), wave % w.kq, blocks, lane)
+                                       : OneRow{};
+  mx_f4 acc[1][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}};
+  one_units<MX_BF16, true, 1, ONE_DOWN_WAVES>(
+      h_hi, h_lo, first, row_at,
+      [&](int slot, int) __attribute__((always_inline)) { return (int64_t)ids[slot] * (H / kMxPanel) + blockIdx.x; },
+      true, k, w, blocks, wave, lane, rows[wave], acc);
   share_sums<1, 1>(part, acc, wave, lane);
   if (wave == 0 && (lane & 15) == 0)
-    *reinterpret_cast<uint2*>(y + blockIdx.x * kMxPanel + 4 * g) = mx_pack4<DT>(total<1, 1>(part, 0, ONE_WAVES, lane));
+    *reinterpret_cast<uint2*>(y + blockIdx.x * kMxPanel + 4 * (lane >> 4)) =
+        mx_pack4<DT>(total<1, 1>(part, 0, ONE_DOWN_WAVES, lane));
 }
 
 // ---------------------------------------------------------------- launches
@@ -596,10 +727,10 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   if (T == 1) {
     err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4)), dim3(256), stream, xp, rp, h, e, sums);
     if (err != hipSuccess) return err;
-    err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k), dim3(UP_WAVES * 64), stream, xp, gate_up, csums, e,
+    err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k), dim3(ONE_UP_WAVES * 64), stream, xp, gate_up, csums, e,
                     kk, renorm, h_blocks, i, ids, weights, hi, lo);
     if (err != hipSuccess) return err;
-    return mx_launch(mx_one_down_kernel<DT>, dim3(panels), dim3(ONE_WAVES * 64), stream, chi, clo, down, cids, kk, i, h,
+    return mx_launch(mx_one_down_kernel<DT>, dim3(panels), dim3(ONE_DOWN_WAVES * 64), stream, chi, clo, down, cids, kk, i, h,
                      yp);
   }
   err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, xp, ldx, rp, h, e, kk,
