@@ -95,7 +95,6 @@ struct Choice {                                 // of the wave's own, in LDS
 // How many of the first n lanes are ahead of each lane.
 __device__ __forceinline__ int lanes_ahead(uint32_t key, int n, int lane) {
   int ahead = 0;
-#pragma unroll 4
   for (int j = 0; j < n; ++j) {
     const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key, j);
     ahead += other > key || (other == key && j < lane);
