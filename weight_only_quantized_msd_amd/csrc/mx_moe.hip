@@ -393,12 +393,14 @@ __device__ __forceinline__ mx_f4 total(const mx_f4* part, int i, int waves, int 
 
 // h of `rows` pairs from `first` on, for Q panels of 16 rows of I; UP_WAVES waves.
 constexpr int UP_WAVES = 4;
-template <int DT, int MT, int Q, typename RowAt, typename PairOf, typename ShareOf>
+template <int DT, int MT, int Q, bool STAGED, typename RowAt, typename PairOf, typename ShareOf>
 __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& row_at, PairOf&& pair_of,
                                         ShareOf&& share_of, const MxTiled& w, int expert, int rows, int blocks, int I,
-                                        int wave, int lane, mx_f4* part, uint16_t* __restrict__ h_hi,
+                                        int wave, int lane, uint8_t* lds, uint16_t* __restrict__ h_hi,
                                         uint16_t* __restrict__ h_lo) {
   constexpr int P = 2 * Q;                        // gate panels, then up panels
+  uint8_t* const xs = lds + wave * STAGE_BYTES;
+  mx_f4* const part = reinterpret_cast<mx_f4*>(lds);
   int64_t panel[P];
   uint32_t f16 = kMxFlagF16;
 #pragma unroll
@@ -413,9 +415,9 @@ __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& 
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
   if (DT == MX_BF16 || f16)
-    expert_units<DT, Rows::kAsIs, MT, P, false>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, nullptr, acc);
+    expert_units<DT, Rows::kAsIs, MT, P, STAGED>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
   else
-    expert_units<DT, Rows::kSplit, MT, P, false>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, nullptr, acc);
+    expert_units<DT, Rows::kSplit, MT, P, STAGED>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
   share_sums<P, MT>(part, acc, wave, lane);
   for (int qm = wave; qm < Q * MT; qm += UP_WAVES) {
     const int i = qm % MT * 16 + (lane & 15);
@@ -427,14 +429,14 @@ __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& 
 }
 
 // Workgroup (Q panels of 16 rows of I, slot): h for all pairs of the slot's expert.
-template <int DT, int Q>
+template <int DT, int Q, bool STAGED>
 __global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                                  MxTiled w, const int32_t* __restrict__ ids,
                                                                  const float* __restrict__ weights, int pairs, int E,
                                                                  int k, int blocks, int I,
                                                                  uint16_t* __restrict__ h_hi,
                                                                  uint16_t* __restrict__ h_lo) {
-  __shared__ mx_f4 part[UP_WAVES * 4 * Q * 64];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[UP_WAVES * (STAGED ? STAGE_BYTES : 4 * Q * 1024)];
   __shared__ uint16_t lists[UP_WAVES][kMoeMaxT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -445,11 +447,11 @@ __global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t
   count = __builtin_amdgcn_readfirstlane(count);
   auto rows_from = [&](auto mt_c, int first) __attribute__((always_inline)) {
     constexpr int MT = decltype(mt_c)::value;
-    up_rows<DT, MT, Q>(
+    up_rows<DT, MT, Q, STAGED>(
         x, [&](int i) __attribute__((always_inline)) { return (int64_t)(list[first + i] / k) * ldx; },
         [&](int i) __attribute__((always_inline)) { return (int)list[first + i]; },
         [&](int i) __attribute__((always_inline)) { return weights[list[first + i]]; }, w, expert,
-        min(count - first, MT * 16), blocks, I, wave, lane, part, h_hi, h_lo);
+        min(count - first, MT * 16), blocks, I, wave, lane, lds, h_hi, h_lo);
   };
   int first = 0;
   for (; count - first > 16; first += 32) {
@@ -740,10 +742,13 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
     return mx_launch(kernel, dim3((rows + q - 1) / q, slots), dim3(UP_WAVES * 64), stream, xp, ldx, gate_up, cids,
                      cweights, pairs, e, kk, h_blocks, i, hi, lo);
   };
-  // two pairs of panels halve the loads of x, which count from about 16 rows an
+  // Two pairs of panels halve the loads of x, which count from about 16 rows an
   // expert (us of the layer with one and two: 32 x 2048 x 2048, 16 experts, 8 of
-  // them chosen 57 and 52; 33 x 1056 x 736, 12, 3: 20.9 and 21.6)
-  err = T * k >= 16 * E ? up(mx_moe_up_kernel<DT, 2>, 2) : up(mx_moe_up_kernel<DT, 1>, 1);
+  // them chosen 57 and 52; 33 x 1056 x 736, 12, 3: 20.9 and 21.6); staged rows then
+  // pay too (direct and staged: 64 x 4096 x 4096, 4, 2: 63.5 and 59.4; 48 x 2048 x
+  // 1024, 16, 8: 49.9 and 47.6; 64 x 1056 x 736, 12, 3: 23.4 and 23.9), but not
+  // below (16 x 4096 x 11008, 8, 2: the product alone 77 and 111).
+  err = T * k >= 16 * E ? up(mx_moe_up_kernel<DT, 2, true>, 2) : up(mx_moe_up_kernel<DT, 1, false>, 1);
   if (err != hipSuccess) return err;
   auto go = [&](auto* kernel, unsigned p, unsigned threads) {
     return mx_launch(kernel, dim3((panels + p - 1) / p, slots), dim3(threads), stream, chi, clo, down, cids, pairs, e, i,
