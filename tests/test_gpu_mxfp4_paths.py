@@ -127,10 +127,11 @@ def clear_case(torch, T, H, inter, E, k, dtype, seed):
     return x, xe, router, re, random_weights(rng, (E, 2 * inter, H)), random_weights(rng, (E, H, inter))
 
 
-MOE = [  # T, H, I, E, k: one token; all rows with the same experts; staged and direct rows; slots by pair and by expert
+MOE = [  # T, H, I, E, k: tokens by themselves and together; all rows with the same experts; staged and direct rows; slots by pair and by expert
     (1, 96, 64, 256, 16), (1, 2080, 1056, 3, 3), (1, 512, 2592, 70, 1), (64, 96, 2080, 2, 2), (64, 160, 96, 1, 1),
     (50, 64, 2208, 3, 1), (20, 2048, 64, 40, 4), (64, 2080, 32, 33, 2), (2, 4096, 32, 200, 16), (5, 1056, 4128, 6, 2),
-    (33, 544, 1056, 4, 3),
+    (33, 544, 1056, 4, 3), (64, 224, 96, 5, 2), (64, 320, 64, 2, 1), (40, 416, 32, 16, 3), (17, 736, 96, 256, 8),
+    (16, 1056, 96, 90, 4), (16, 768, 96, 90, 6), (9, 1184, 2080, 12, 1), (24, 512, 224, 4, 1),
 ]
 
 
@@ -150,7 +151,7 @@ def test_moe_paths(torch, renorm, dtype, T, H, inter, E, k):
     assert same(torch, y, again[0]) and torch.equal(got_ids, again[1]) and same(torch, got_weights, again[2])
 
 
-@pytest.mark.parametrize("T,H,inter,E,k", [(40, 64, 96, 6, 2), (40, 64, 2080, 6, 2), (1, 64, 96, 6, 2)])
+@pytest.mark.parametrize("T,H,inter,E,k", [(40, 64, 96, 6, 2), (40, 64, 2080, 6, 2), (1, 64, 96, 6, 2), (40, 384, 96, 6, 2), (40, 384, 2080, 6, 2)])
 def test_moe_a_nan_weight_stays_with_its_expert(torch, T, H, inter, E, k):
     import weight_only_quantized_msd_amd as W
     x, xe, router, re, gu, dn = clear_case(torch, T, H, inter, E, k, "bf16", 21)
@@ -173,12 +174,12 @@ def test_moe_a_nan_weight_stays_with_its_expert(torch, T, H, inter, E, k):
 
 @pytest.mark.parametrize("values", ["few", "special", "equal"])
 @pytest.mark.parametrize("E,k", [(1, 1), (7, 7), (32, 16), (33, 5), (64, 16), (65, 1), (65, 16), (128, 8), (200, 16), (256, 16)])
-@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("T", [1, 2, 64])
 def test_moe_choices(torch, T, E, k, values):
     """Larger logits first, NaN above all, -0 equal to +0, equal logits by index; the logits are exact."""
     import weight_only_quantized_msd_amd as W
     rng = np.random.default_rng(E + k)
-    H, inter = 64, 32
+    H, inter = 64 if T < 64 else 224, 32        # 64 tokens of 224: together
     of = {"few": [-1.0, -0.0, 0.0, 0.5, 3.0], "special": [-np.inf, -2.0, -0.0, 0.0, 1.0, np.inf, np.nan], "equal": [-1.5]}
     logits = rng.choice(of[values], E)
     x, router = np.zeros((T, H)), np.zeros((E, H))

@@ -1,5 +1,5 @@
 // mx_moe.hip -- a mixture-of-experts layer with MXFP4 experts for up to 64
-// tokens, in four launches (three for one token):
+// tokens, in four launches:
 //   route: logits = router . x, softmax, the k largest per token;
 //   up:    h = weight * silu(gate_e . x) * (up_e . x) for every (token, choice)
 //          pair, a workgroup for a reached expert and one or two panels of 16
@@ -15,7 +15,10 @@
 // Bound by the weights: 16 tokens, H = 4096, I = 11008, 8 experts, 2 chosen: route
 // 6 us, up 76 (383 MB, 5.0 TB/s), down 40 (191 MB, 4.8 TB/s), sum 4.  Small layers
 // are bound by the chain of launches and trips to memory: 33 tokens, H = 1056, I =
-// 736, 12 experts, 3 chosen: 4.6 + 7.6 + 5.7 + 2.6 us.
+// 736, 12 experts, 3 chosen: 4.5 + 7.5 + 5.1 + 2.4 us.
+//
+// One token, and few, are taken by themselves in three launches, at the end of
+// this file: 1 token, H = 2048, I = 1024, 64 experts, 8 chosen: 2.6 + 8.2 + 4.4 us.
 #include <algorithm>
 
 #include "mx_tile.hpp"
@@ -526,21 +529,21 @@ __global__ __launch_bounds__(256) void mx_moe_sum_kernel(const float* __restrict
   reinterpret_cast<uint2*>(y)[i] = mx_pack4<DT>(v);
 }
 
-// ---------------------------------------------------------------- one token
-// Its choices are the k slots.  The logits come from many workgroups (a single
-// one reads the router at some 100 GB/s), each workgroup of the gate and up
-// product then chooses by itself, and one workgroup adds all experts' shares of
-// its columns of y.
+// ---------------------------------------------------------------- tokens by themselves
+// One token, or few (by_token): its choices are the k slots, and nothing is shared
+// between tokens.  The logits come from many workgroups (a single one reads the
+// router at some 100 GB/s), each workgroup of the gate and up product then chooses
+// by itself, and one workgroup adds all experts' shares of its columns of y.
 constexpr int ONE_UP_WAVES = 4, ONE_DOWN_WAVES = 16;
 template <int DT>
-__global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __restrict__ x,
+__global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                             const uint16_t* __restrict__ router, int H, int E,
                                                             float* __restrict__ logits) {
   const int lane = threadIdx.x & 63;
   const int e = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float s[1];
-  router_logits<DT, 1>(reinterpret_cast<const uint4*>(x), router, H, E, e, lane, s);
-  if (lane == 0 && e < E) logits[e] = s[0];
+  router_logits<DT, 1>(reinterpret_cast<const uint4*>(x + blockIdx.y * ldx), router, H, E, e, lane, s);
+  if (lane == 0 && e < E) logits[blockIdx.y * E + e] = s[0];
 }
 
 // A unit of a row, 512 values from 512 * q on: 16 bytes a lane.  In h chunk
@@ -636,10 +639,10 @@ __device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, cons
   }
 }
 
-// Workgroup: a panel of 16 rows of I, one choice.
+// Workgroup: a panel of 16 rows of I, one choice of one token.
 template <int DT>
-__global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint16_t* __restrict__ x, MxTiled w,
-                                                                     const float* __restrict__ logits, int E, int k,
+__global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                                     MxTiled w, const float* __restrict__ logits, int E, int k,
                                                                      int renormalize, int blocks, int I,
                                                                      int32_t* __restrict__ ids,
                                                                      float* __restrict__ weights,
@@ -650,32 +653,33 @@ __global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint
   __shared__ Choice choices[ONE_UP_WAVES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const OneRow first = one_row<false>(x, x, 0, wave, blocks, lane);
+  const int64_t t = blockIdx.z;
+  const OneRow first = one_row<false>(x, x, t * ldx, wave, blocks, lane);
   int id;
   float mine, sum;
-  choose(logits, choices[wave], E, k, renormalize != 0, lane, id, mine, sum);
+  choose(logits + t * E, choices[wave], E, k, renormalize != 0, lane, id, mine, sum);
   const int slot = blockIdx.y, expert = __builtin_amdgcn_readlane(id, slot), half = I / kMxPanel;
   const int64_t panel = (int64_t)expert * (2 * half) + blockIdx.x;
   const bool exact = DT == MX_BF16 || (w.flags[panel] & w.flags[panel + half] & kMxFlagF16) != 0;
   mx_f4 acc[2][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}, {mx_f4{0.f, 0.f, 0.f, 0.f}}};
   one_units<DT, false, 2, ONE_UP_WAVES>(
-      x, x, first, [](int) __attribute__((always_inline)) { return (int64_t)0; },
+      x, x, first, [&](int) __attribute__((always_inline)) { return t * ldx; },
       [&](int, int p) __attribute__((always_inline)) { return panel + p * half; }, exact, 1, w, blocks, wave, lane,
       rows[wave], acc);
   share_sums<2, 1>(part, acc, wave, lane);
   if (wave != 0) return;
   const float weight = mine / wave_sum(sum), share = __shfl(weight, slot);
   if (blockIdx.x == 0 && slot == 0 && lane < k) {
-    ids[lane] = id;
-    weights[lane] = weight;
+    ids[t * k + lane] = id;
+    weights[t * k + lane] = weight;
   }
   if ((lane & 15) == 0) {
     const mx_f4 a = total<2, 1>(part, 0, ONE_UP_WAVES, lane), b = total<2, 1>(part, 1, ONE_UP_WAVES, lane);
-    store_h(h_hi, h_lo, slot * h_pitch(I) + h_place(blockIdx.x * kMxPanel + 4 * (lane >> 4)), gated(a, b, share));
+    store_h(h_hi, h_lo, (t * k + slot) * h_pitch(I) + h_place(blockIdx.x * kMxPanel + 4 * (lane >> 4)), gated(a, b, share));
   }
 }
 
-// Workgroup: a panel of 16 columns of y, all choices.
+// Workgroup: a panel of 16 columns of y, all choices of one token.
 template <int DT>
 __global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h_hi,
                                                                          const uint16_t* __restrict__ h_lo, MxTiled w,
@@ -685,26 +689,40 @@ __global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const 
   __shared__ uint4 rows[ONE_DOWN_WAVES][2 * 64];
   const int lane = threadIdx.x & 63, blocks = I / kMxBlock;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  auto row_at = [&](int slot) __attribute__((always_inline)) { return slot * h_pitch(I); };
+  const int64_t t = blockIdx.y;
+  auto row_at = [&](int slot) __attribute__((always_inline)) { return (t * k + slot) * h_pitch(I); };
   const OneRow first = wave < k * w.kq ? one_row<true>(h_hi, h_lo, row_at(wave / w.kq), wave % w.kq, blocks, lane)
                                        : OneRow{};
   mx_f4 acc[1][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}};
   one_units<MX_BF16, true, 1, ONE_DOWN_WAVES>(
       h_hi, h_lo, first, row_at,
-      [&](int slot, int) __attribute__((always_inline)) { return (int64_t)ids[slot] * (H / kMxPanel) + blockIdx.x; },
+      [&](int slot, int) __attribute__((always_inline)) { return (int64_t)ids[t * k + slot] * (H / kMxPanel) + blockIdx.x; },
       true, k, w, blocks, wave, lane, rows[wave], acc);
   share_sums<1, 1>(part, acc, wave, lane);
   if (wave == 0 && (lane & 15) == 0)
-    *reinterpret_cast<uint2*>(y + blockIdx.x * kMxPanel + 4 * (lane >> 4)) =
+    *reinterpret_cast<uint2*>(y + t * H + blockIdx.x * kMxPanel + 4 * (lane >> 4)) =
         mx_pack4<DT>(total<1, 1>(part, 0, ONE_DOWN_WAVES, lane));
 }
 
 // ---------------------------------------------------------------- launches
+// Each token by itself, in three launches, or the experts' pairs together, in
+// four.  By itself every pair reads its expert's weights, which pays while most
+// pairs have experts of their own (T * k <= 3/4 E), or while all that reading is
+// small and the workgroups are few.  us of the layer together and by token (T, H,
+// I, E, k): 2 x 2048 x 1024, 64, 8 28.9 and 18.9; 6: 52.0 and 42.7; 12: 64.6 and
+// 68.2; 16 x 4096 x 1024, 256, 8 211 and 182; 3 x 4096 x 4096, 16, 4 69.5 and 70.9,
+// 4: 78.1 and 86.7; 6 x 1056 x 736, 12, 3 17.7 and 16.5, 8: 18.3 and 20.1; 24 x 512 x
+// 256, 4, 1 13.8 and 13.0, 32: 14.1 and 14.3; 24 x 1024 x 256, 64, 1 15.9 and 18.5.
+static bool by_token(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+  if (T == 1) return true;
+  return (T <= 16 && 4 * T * k <= 3 * E) || (T * H <= 12288 && T * k * H * I <= (int64_t)14 << 20);
+}
+
 static size_t h_bytes(int64_t T, int64_t I, int64_t k) { return (size_t)(T * k * h_pitch(I) * 2); }
 
-// h in two parts, then the pairs' shares of y (more than one token) or the logits (one).
+// h in two parts, then the pairs' shares of y or the tokens' logits (by_token).
 size_t mx_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t k) {
-  return 2 * h_bytes(T, I, k) + (T == 1 ? kMoeMaxE * 4 : (size_t)(T * k * H * 4));
+  return 2 * h_bytes(T, I, k) + (size_t)(T * std::max<int64_t>(kMoeMaxE, k * H) * 4);
 }
 
 template <int DT>
@@ -725,14 +743,16 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   auto* csums = static_cast<const float*>(sums);
   const unsigned rows = (unsigned)(I / kMxPanel), panels = (unsigned)(H / kMxPanel);
   hipError_t err;
-  if (T == 1) {
-    err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4)), dim3(256), stream, xp, rp, h, e, sums);
+  if (by_token(T, H, I, E, k)) {
+    const unsigned t = (unsigned)T;
+    err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4), t), dim3(256), stream, xp, ldx, rp, h, e,
+                    sums);
     if (err != hipSuccess) return err;
-    err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k), dim3(ONE_UP_WAVES * 64), stream, xp, gate_up, csums, e,
-                    kk, renorm, h_blocks, i, ids, weights, hi, lo);
+    err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k, t), dim3(ONE_UP_WAVES * 64), stream, xp, ldx, gate_up,
+                    csums, e, kk, renorm, h_blocks, i, ids, weights, hi, lo);
     if (err != hipSuccess) return err;
-    return mx_launch(mx_one_down_kernel<DT>, dim3(panels), dim3(ONE_DOWN_WAVES * 64), stream, chi, clo, down, cids, kk, i, h,
-                     yp);
+    return mx_launch(mx_one_down_kernel<DT>, dim3(panels, t), dim3(ONE_DOWN_WAVES * 64), stream, chi, clo, down, cids,
+                     kk, i, h, yp);
   }
   err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, xp, ldx, rp, h, e, kk,
                   renorm, ids, weights);
