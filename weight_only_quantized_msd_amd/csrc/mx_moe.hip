@@ -249,7 +249,7 @@ __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int p
 //     whole rows a copy, the 16-byte chunks of a row permuted (chunk ^ row % 16);
 //   direct: each lane loads its 16-byte operands, which touches a cache line a
 //     lane, but needs no LDS, so more workgroups share a CU.
-// Staged is for experts with more than a few rows (launch_mx_moe's rule).
+// Staged is for experts with more than a few rows (moe_dt's rules).
 enum class Rows { kAsIs, kSplit, kPair };      // 16-bit; fp16 as two bf16; bf16 pairs (h)
 constexpr int STAGE_BYTES = 16 * 1024;
 
