@@ -220,9 +220,9 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64) void mx_route_kernel(const uint16
 // Which expert a slot stands for: where there are fewer pairs (token * k +
 // choice) than experts, slot i is pair i's expert, if no pair before i has the
 // same; else slot i is expert i.  `list` (LDS of this wave's own, T entries)
-// gets the expert's pairs in ascending order.  Returns the expert, or -1 if the
-// slot is empty.  Each wave does this by itself: no barrier stands between the
-// ids and the first load of weights.
+// gets the expert's pairs in ascending order, for all lanes.  Returns the expert,
+// or -1 if the slot is empty.  Each wave does this by itself: no barrier stands
+// between the ids and the first load of weights.
 __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int pairs, int E, int slot, int lane,
                                           uint16_t* list, int& count) {
   const bool by_pair = pairs < E;
@@ -237,6 +237,7 @@ __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int p
     if (by_pair && n == 0 && votes != 0) mine = p0 + __ffsll((unsigned long long)votes) - 1 == slot;
     n += __popcll(votes);
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // lanes read what others wrote
   count = n;
   return n > 0 && mine ? expert : -1;
 }
