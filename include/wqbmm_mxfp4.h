@@ -95,7 +95,7 @@ wqbmm_status wqbmm_mxfp4_matmul(const void* x, int dtype, int64_t ldx, const voi
  * logits (ties to the lowest index; a NaN counts as the largest); their
  * softmax probabilities over all E experts, divided by their sum if
  * renormalize != 0; y = sum over them of weight * down_e . (silu(gate_e . x)
- * * (up_e . x)).  Intermediate values keep 16 significant bits.
+ * * (up_e . x)).  Intermediate values keep fp32's 24 bits.
  * Rules: H, I multiples of 32; 1 <= E <= 256; 1 <= k <= min(E, 16);
  * E * 2I and E * H at most 2^24.  More tokens: WQBMM_ERR_INVALID.
  */

@@ -170,4 +170,25 @@ __device__ __forceinline__ void mx_split8(uint4 v, uint4& hi, uint4& lo) {
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// Four fp32 values as the sum of three bf16 parts each, packed: 24 significant
+// bits are eight, eight and eight, cut off and not rounded, so that no part is
+// larger than the value (below 2^-110 the last part loses bits that bf16 does not
+// have).  An infinity has rests 0 (inf - inf would be NaN).
+__device__ __forceinline__ void mx_split24(mx_f4 v, uint2 (&part)[3]) {
+  uint32_t o[3][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      o[n][i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);           // the upper halves
+      a = __builtin_isinf(a) ? 0.0f : a - __uint_as_float(ua & 0xffff0000u);
+      b = __builtin_isinf(b) ? 0.0f : b - __uint_as_float(ub & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 3; ++n) part[n] = make_uint2(o[n][0], o[n][1]);
+}
+
 }  // namespace wqbmm

@@ -251,25 +251,24 @@ __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int p
 //   direct: each lane loads its 16-byte operands, which touches a cache line a
 //     lane, but needs no LDS, so more workgroups share a CU.
 // Staged is for experts with more than a few rows (moe_dt's rules).
-enum class Rows { kAsIs, kSplit, kPair };      // 16-bit; fp16 as two bf16; bf16 pairs (h)
-constexpr int STAGE_BYTES = 16 * 1024;
+enum class Rows {
+  kAsIs,       // 16-bit
+  kSplit,      // fp16 as two bf16
+  kParts,      // h's three parts, added in the accumulators
+  kPartRows    // h's parts as rows of their own
+};
+constexpr int PART_BYTES = 8 * 1024;           // staged rows of a wave: two of these, three for kParts
 
-// 16 significant bits of h: two bf16 parts, whose products with the weights
-// are exact, and which keep fp32's range (h in fp16 would overflow early, in
-// bf16 alone it would cost as much as the output's own rounding).
-__device__ __forceinline__ void store_h(uint16_t* __restrict__ hi, uint16_t* __restrict__ lo, int64_t at, mx_f4 v) {
-  uint32_t h[2], l[2];
+// h goes from one product to the other in 24 bits, fp32's, as three bf16 parts,
+// whose products with the weights are exact, at h, h + part and h + 2 * part.  (In
+// two parts, 16 bits, the layer's outputs were 1.1e-4 of their norm away from sums
+// in fp32 at 16 x 4096 x 11008, 8 experts, 2 chosen, and are 0.6e-4 now; the layer
+// took 129 us.  h in fp32, cut by the down product, took 144.)
+__device__ __forceinline__ void store_h(uint16_t* __restrict__ h, int64_t part, int64_t at, mx_f4 v) {
+  uint2 o[3];
+  mx_split24(v, o);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const mx_bf2 b = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
-    h[i] = __builtin_bit_cast(uint32_t, b);
-    const float h0 = mx_lo<MX_BF16>(h[i]), h1 = mx_hi<MX_BF16>(h[i]);
-    const mx_bf2 r = {(__bf16)(__builtin_isfinite(h0) ? v[2 * i] - h0 : 0.0f),
-                      (__bf16)(__builtin_isfinite(h1) ? v[2 * i + 1] - h1 : 0.0f)};
-    l[i] = __builtin_bit_cast(uint32_t, r);
-  }
-  *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
-  *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
+  for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2*>(h + n * part + at) = o[n];
 }
 
 // share * silu(a) * b
@@ -290,18 +289,19 @@ __device__ __forceinline__ int h_place(int i) {
   return (i & ~127) | ((i & 24) << 2) | ((i & 96) >> 2) | (i & 7);
 }
 
-// row_at(i): the first value of row i, as an offset into `src` (and `src_lo`).
+// row_at(i): the first value of row i, as an offset into `src`; h's parts are
+// `part` values apart.
 template <int DT, Rows MODE, int MT, int P, bool STAGED, typename RowAt>
-__device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
-                                             RowAt&& row_at, const MxTiled& w, const int64_t (&panel)[P], int rows,
-                                             int blocks, int wave, int waves, int lane, uint8_t* xs,
-                                             mx_f4 (&acc)[P][MT]) {
-  constexpr bool PAIR = MODE == Rows::kPair;
-  constexpr int U = STAGED ? (PAIR ? 2 : 4) / MT : 4;
-  constexpr int LANES = 16 * U, ROWS = 64 / LANES, LO = STAGE_BYTES / 2;
+__device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, int64_t part, RowAt&& row_at,
+                                             const MxTiled& w, const int64_t (&panel)[P], int rows, int blocks,
+                                             int wave, int waves, int lane, uint8_t* xs, mx_f4 (&acc)[P][MT]) {
+  constexpr bool H = MODE == Rows::kParts || MODE == Rows::kPartRows;
+  constexpr int PARTS = MODE == Rows::kParts ? 3 : 1, TERMS = MODE == Rows::kSplit ? 2 : PARTS;
+  constexpr int U = !H ? (STAGED ? 4 / MT : 4) : STAGED ? 2 / MT : 2;
+  constexpr int LANES = 16 * U, ROWS = 64 / LANES;
   constexpr int CT = MODE == Rows::kAsIs ? DT : MX_BF16;
   const int r = lane & 15, g = lane >> 4;
-  auto chunk_of = [&](int i, int j) __attribute__((always_inline)) { return PAIR ? 16 * i + 4 * j + g : 16 * i + 4 * g + j; };
+  auto chunk_of = [&](int i, int j) __attribute__((always_inline)) { return H ? 16 * i + 4 * j + g : 16 * i + 4 * g + j; };
   for (int kt = wave * U; kt < w.kt; kt += waves * U) {
     if constexpr (STAGED) {
       mx_wait_lds();                              // the last unit's reads, before its rows are overwritten
@@ -310,10 +310,11 @@ __device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, c
         if (i * ROWS >= rows) break;
         const int row = i * ROWS + lane / LANES;
         const int chunk = kt * 16 + ((lane % LANES) ^ (row & 15));
-        const bool in = chunk < (PAIR ? w.kt * 16 : blocks * 4);
-        const int64_t at = row_at(min(row, rows - 1)) + (in ? chunk * 8 : 0);
-        __builtin_amdgcn_global_load_lds(src + at, xs + i * 1024, 16, 0, 0);
-        if constexpr (PAIR) __builtin_amdgcn_global_load_lds(src_lo + at, xs + LO + i * 1024, 16, 0, 0);
+        const bool in = chunk < (H ? w.kt * 16 : blocks * 4);
+        const uint16_t* const from = src + row_at(min(row, rows - 1)) + (in ? chunk * 8 : 0);
+#pragma unroll
+        for (int n = 0; n < PARTS; ++n)
+          __builtin_amdgcn_global_load_lds(from + n * part, xs + n * PART_BYTES + i * 1024, 16, 0, 0);
       }
     }
     uint4 c[P][U];
@@ -332,44 +333,45 @@ __device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, c
       const bool whole = 4 * (kt + i) + 4 <= blocks, in = 4 * (kt + i) + g < blocks;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        uint4 v[4], l[4];
+        uint4 v[4][TERMS];
         if constexpr (STAGED) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint8_t* const at = xs + (mt * 16 + r) * (LANES * 16) + (chunk_of(i, j) ^ r) * 16;
-            v[j] = *reinterpret_cast<const uint4*>(at);
-            if constexpr (PAIR) l[j] = *reinterpret_cast<const uint4*>(at + LO);
-          }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int n = 0; n < PARTS; ++n)
+              v[j][n] = *reinterpret_cast<const uint4*>(xs + n * PART_BYTES + (mt * 16 + r) * (LANES * 16) +
+                                                        (chunk_of(i, j) ^ r) * 16);
           if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = in ? v[j] : make_uint4(0u, 0u, 0u, 0u);
-              if constexpr (PAIR) l[j] = in ? l[j] : make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < PARTS; ++n) v[j][n] = in ? v[j][n] : make_uint4(0u, 0u, 0u, 0u);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = l[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (mt * 16 + r < rows && in) {
-            const int64_t at = row_at(mt * 16 + r) + kt * kMxTile;
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = *reinterpret_cast<const uint4*>(src + at + chunk_of(i, j) * 8);
-              if constexpr (PAIR) l[j] = *reinterpret_cast<const uint4*>(src_lo + at + chunk_of(i, j) * 8);
-            }
+            for (int n = 0; n < PARTS; ++n) v[j][n] = make_uint4(0u, 0u, 0u, 0u);
+          if (mt * 16 + r < rows && in) {
+            const uint16_t* const from = src + row_at(mt * 16 + r) + kt * kMxTile;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < PARTS; ++n)
+                v[j][n] = *reinterpret_cast<const uint4*>(from + n * part + chunk_of(i, j) * 8);
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if constexpr (MODE == Rows::kSplit) {
-            const uint4 both = v[j];
-            mx_split8(both, v[j], l[j]);
+            const uint4 both = v[j][0];
+            mx_split8(both, v[j][0], v[j][1]);
           }
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             const uint4 a = mx_decode8<CT>(dword_of(c[p][i], j), mx_scale((sc[p] >> (8 * i)) & 0xffu));
-            acc[p][mt] = mx_mfma16<CT>(a, v[j], acc[p][mt]);
-            if constexpr (MODE != Rows::kAsIs) acc[p][mt] = mx_mfma16<CT>(a, l[j], acc[p][mt]);
+#pragma unroll
+            for (int n = 0; n < TERMS; ++n) acc[p][mt] = mx_mfma16<CT>(a, v[j][n], acc[p][mt]);
           }
         }
       }
@@ -400,11 +402,10 @@ constexpr int UP_WAVES = 4;
 template <int DT, int MT, int Q, bool STAGED, typename RowAt, typename PairOf, typename ShareOf>
 __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& row_at, PairOf&& pair_of,
                                         ShareOf&& share_of, const MxTiled& w, int expert, int rows, int blocks, int I,
-                                        int wave, int lane, uint8_t* lds, uint16_t* __restrict__ h_hi,
-                                        uint16_t* __restrict__ h_lo) {
+                                        int wave, int lane, uint8_t* lds, uint16_t* __restrict__ h, int64_t part) {
   constexpr int P = 2 * Q;                        // gate panels, then up panels
-  uint8_t* const xs = lds + wave * STAGE_BYTES;
-  mx_f4* const part = reinterpret_cast<mx_f4*>(lds);
+  uint8_t* const xs = lds + wave * (2 * PART_BYTES);
+  mx_f4* const sums = reinterpret_cast<mx_f4*>(lds);
   int64_t panel[P];
   uint32_t f16 = kMxFlagF16;
 #pragma unroll
@@ -419,28 +420,27 @@ __device__ __forceinline__ void up_rows(const uint16_t* __restrict__ x, RowAt&& 
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
   if (DT == MX_BF16 || f16)
-    expert_units<DT, Rows::kAsIs, MT, P, STAGED>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
+    expert_units<DT, Rows::kAsIs, MT, P, STAGED>(x, 0, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
   else
-    expert_units<DT, Rows::kSplit, MT, P, STAGED>(x, x, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
-  share_sums<P, MT>(part, acc, wave, lane);
+    expert_units<DT, Rows::kSplit, MT, P, STAGED>(x, 0, row_at, w, panel, rows, blocks, wave, UP_WAVES, lane, xs, acc);
+  share_sums<P, MT>(sums, acc, wave, lane);
   for (int qm = wave; qm < Q * MT; qm += UP_WAVES) {
     const int i = qm % MT * 16 + (lane & 15);
     const int at = (blockIdx.x * Q + qm / MT) * kMxPanel + 4 * (lane >> 4);
     if (i >= rows || at >= I) continue;
-    const mx_f4 a = total<P, MT>(part, qm, UP_WAVES, lane), b = total<P, MT>(part, Q * MT + qm, UP_WAVES, lane);
-    store_h(h_hi, h_lo, pair_of(i) * h_pitch(I) + h_place(at), gated(a, b, share_of(i)));
+    const mx_f4 a = total<P, MT>(sums, qm, UP_WAVES, lane), b = total<P, MT>(sums, Q * MT + qm, UP_WAVES, lane);
+    store_h(h, part, pair_of(i) * h_pitch(I) + h_place(at), gated(a, b, share_of(i)));
   }
 }
 
 // Workgroup (Q panels of 16 rows of I, slot): h for all pairs of the slot's expert.
+// Direct: four waves a SIMD, i.e. at most 128 registers.
 template <int DT, int Q, bool STAGED>
-__global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                                 MxTiled w, const int32_t* __restrict__ ids,
-                                                                 const float* __restrict__ weights, int pairs, int E,
-                                                                 int k, int blocks, int I,
-                                                                 uint16_t* __restrict__ h_hi,
-                                                                 uint16_t* __restrict__ h_lo) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[UP_WAVES * (STAGED ? STAGE_BYTES : 4 * Q * 1024)];
+__global__ __launch_bounds__(UP_WAVES * 64, STAGED ? 1 : 4) void mx_moe_up_kernel(
+    const uint16_t* __restrict__ x, int64_t ldx, MxTiled w, const int32_t* __restrict__ ids,
+    const float* __restrict__ weights, int pairs, int E, int k, int blocks, int I, uint16_t* __restrict__ h,
+    int64_t part) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[UP_WAVES * (STAGED ? 2 * PART_BYTES : 4 * Q * 1024)];
   __shared__ uint16_t lists[UP_WAVES][kMoeMaxT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t
         x, [&](int i) __attribute__((always_inline)) { return (int64_t)(list[first + i] / k) * ldx; },
         [&](int i) __attribute__((always_inline)) { return (int)list[first + i]; },
         [&](int i) __attribute__((always_inline)) { return weights[list[first + i]]; }, w, expert,
-        min(count - first, MT * 16), blocks, I, wave, lane, lds, h_hi, h_lo);
+        min(count - first, MT * 16), blocks, I, wave, lane, lds, h, part);
   };
   int first = 0;
   for (; count - first > 16; first += 32) {
@@ -465,21 +465,30 @@ __global__ __launch_bounds__(UP_WAVES * 64) void mx_moe_up_kernel(const uint16_t
   if (first < count) rows_from(std::integral_constant<int, 1>{}, first);
 }
 
-// Workgroup (P panels of 16 columns of y, slot): the expert's share of y, fp32,
-// for each of its pairs.
-template <int P, bool STAGED>
-__global__ __launch_bounds__(STAGED ? 512 : 256) void mx_moe_down_kernel(const uint16_t* __restrict__ h_hi,
-                                                                        const uint16_t* __restrict__ h_lo, MxTiled w,
-                                                                        const int32_t* __restrict__ ids, int pairs,
-                                                                        int E, int I, int H,
-                                                                        float* __restrict__ sums) {
-  constexpr int WAVES = STAGED ? 8 : 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGED ? WAVES * STAGE_BYTES : WAVES * 2 * P * 1024];
+// Workgroup (four panels of 16 columns of y, slot): the expert's share of y, fp32,
+// for each of its pairs.  The parts of h are three products for a pair's column; or,
+// for few pairs, three columns of one product, whose sixteen hold five pairs.
+// (Two panels took longer everywhere, direct, us: 48 x 2048 x 1024, 16 experts, 8
+// chosen 26.6 and 18.2; 33 x 1056 x 736, 12, 3: 6.8 and 6.6.)
+constexpr int DOWN_PANELS = 4;
+enum class Down { kDirect, kStaged, kFew };
+constexpr int down_waves(Down kind) { return kind == Down::kDirect ? 4 : kind == Down::kStaged ? 6 : 8; }
+template <Down KIND>
+__global__ __launch_bounds__(down_waves(KIND) * 64) void mx_moe_down_kernel(const uint16_t* __restrict__ h,
+                                                                           int64_t part, MxTiled w,
+                                                                           const int32_t* __restrict__ ids, int pairs,
+                                                                           int E, int I, int H,
+                                                                           float* __restrict__ sums) {
+  constexpr int P = DOWN_PANELS, WAVES = down_waves(KIND);
+  constexpr int MOST = KIND == Down::kFew ? 10 : 32;                     // pairs at a time
+  constexpr int MINE = KIND == Down::kDirect ? 2 * P * 1024 : (KIND == Down::kFew ? 1 : 3) * PART_BYTES;
+  static_assert(MINE >= 2 * P * 1024, "a wave's sums");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * MINE];
   __shared__ uint16_t lists[WAVES][kMoeMaxT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint16_t* const list = lists[wave];
-  mx_f4* const part = reinterpret_cast<mx_f4*>(lds);
+  mx_f4* const shared = reinterpret_cast<mx_f4*>(lds);
   int count = 0;
   const int expert = __builtin_amdgcn_readfirstlane(slot_pairs(ids, pairs, E, blockIdx.y, lane, list, count));
   if (expert < 0) return;
@@ -489,31 +498,52 @@ __global__ __launch_bounds__(STAGED ? 512 : 256) void mx_moe_down_kernel(const u
   for (int p = 0; p < P; ++p)
     panel[p] = (int64_t)expert * (H / kMxPanel) + min((int)blockIdx.x * P + p, H / kMxPanel - 1);
 
-  auto rows_from = [&](auto mt_c, int first) __attribute__((always_inline)) {
+  auto pairs_from = [&](auto mt_c, int first) __attribute__((always_inline)) {
     constexpr int MT = decltype(mt_c)::value;
-    const int rows = min(count - first, MT * 16);
-    auto row_at = [&](int i) __attribute__((always_inline)) { return list[first + i] * h_pitch(I); };
+    const int here = min(count - first, MOST / 2 * MT);
     mx_f4 acc[P][MT];
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) acc[p][mt] = mx_f4{0.f, 0.f, 0.f, 0.f};
-    expert_units<MX_BF16, Rows::kPair, MT, P, STAGED>(h_hi, h_lo, row_at, w, panel, rows, I / kMxBlock, wave, WAVES,
-                                                      lane, lds + wave * STAGE_BYTES, acc);
-    share_sums<P, MT>(part, acc, wave, lane);
-    for (int pm = wave; pm < P * MT; pm += WAVES) {
-      const int i = pm % MT * 16 + (lane & 15);
-      const int n = (blockIdx.x * P + pm / MT) * kMxPanel + 4 * (lane >> 4);
-      const mx_f4 v = total<P, MT>(part, pm, WAVES, lane);
-      if (i < rows && n < H) *reinterpret_cast<mx_f4*>(sums + (int64_t)list[first + i] * H + n) = v;
+    uint8_t* const mine = lds + wave * MINE;
+    if constexpr (KIND == Down::kFew) {                                  // row 3 * i + n is part n of pair i
+      auto row_at = [&](int row) __attribute__((always_inline)) {
+        return list[first + row / 3] * h_pitch(I) + row % 3 * part;
+      };
+      expert_units<MX_BF16, Rows::kPartRows, MT, P, true>(h, 0, row_at, w, panel, 3 * here, I / kMxBlock, wave, WAVES,
+                                                          lane, mine, acc);
+    } else {
+      auto row_at = [&](int i) __attribute__((always_inline)) { return list[first + i] * h_pitch(I); };
+      expert_units<MX_BF16, Rows::kParts, MT, P, KIND == Down::kStaged>(h, part, row_at, w, panel, here, I / kMxBlock,
+                                                                        wave, WAVES, lane, mine, acc);
+    }
+    share_sums<P, MT>(shared, acc, wave, lane);
+    if constexpr (KIND == Down::kFew) {
+      for (int t = threadIdx.x; t < 4 * P * here; t += WAVES * 64) {      // four columns of a pair
+        const int i = t / (4 * P), p = t / 4 % P, g = t % 4;
+        mx_f4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int row = 3 * i; row < 3 * i + 3; ++row)
+          v += total<P, MT>(shared, p * MT + row / 16, WAVES, 16 * g + row % 16);
+        const int n = (blockIdx.x * P + p) * kMxPanel + 4 * g;
+        if (n < H) *reinterpret_cast<mx_f4*>(sums + (int64_t)list[first + i] * H + n) = v;
+      }
+    } else {
+      for (int pm = wave; pm < P * MT; pm += WAVES) {
+        const int i = pm % MT * 16 + (lane & 15);
+        const int n = (blockIdx.x * P + pm / MT) * kMxPanel + 4 * (lane >> 4);
+        const mx_f4 v = total<P, MT>(shared, pm, WAVES, lane);
+        if (i < here && n < H) *reinterpret_cast<mx_f4*>(sums + (int64_t)list[first + i] * H + n) = v;
+      }
     }
   };
   int first = 0;
-  for (; count - first > 16; first += 32) {
-    rows_from(std::integral_constant<int, 2>{}, first);
-    __syncthreads();
+  for (; count - first > MOST / 2; first += MOST) {
+    pairs_from(std::integral_constant<int, 2>{}, first);
+    __syncthreads();                              // the sums are read before they are overwritten
   }
-  if (first < count) rows_from(std::integral_constant<int, 1>{}, first);
+  if (first < count) pairs_from(std::integral_constant<int, 1>{}, first);
 }
 
 // y[t] = the sum of token t's pairs, in order of choice; a thread takes four columns.
@@ -547,41 +577,44 @@ __global__ __launch_bounds__(256) void mx_one_logits_kernel(const uint16_t* __re
   if (lane == 0 && e < E) logits[blockIdx.y * E + e] = s[0];
 }
 
-// A unit of a row, 512 values from 512 * q on: 16 bytes a lane.  In h chunk
-// lane % 16 of a K-tile belongs to block lane % 4 (h_place), in x to block
-// lane % 16 / 4.
+// A unit of a row, 512 values from 512 * q on: 16 bytes a lane (of each of h's
+// three parts).  In h chunk lane % 16 of a K-tile belongs to block lane % 4
+// (h_place), in x to block lane % 16 / 4.
+template <int PARTS>
 struct OneRow {
-  uint4 hi, lo;
+  uint4 v[PARTS];
 };
-template <bool PAIR>
-__device__ __forceinline__ OneRow one_row(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
-                                          int64_t row, int q, int blocks, int lane) {
-  OneRow v = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (4 * (4 * q + (lane >> 4)) + (PAIR ? lane & 3 : (lane >> 2) & 3) < blocks) {
-    const int64_t at = row + (int64_t)q * 4 * kMxTile + lane * 8;
-    v.hi = *reinterpret_cast<const uint4*>(src + at);
-    if constexpr (PAIR) v.lo = *reinterpret_cast<const uint4*>(src_lo + at);
+template <int PARTS>
+__device__ __forceinline__ OneRow<PARTS> one_row(const uint16_t* __restrict__ src, int64_t part, int64_t row, int q,
+                                                 int blocks, int lane) {
+  OneRow<PARTS> o;
+#pragma unroll
+  for (int n = 0; n < PARTS; ++n) o.v[n] = make_uint4(0u, 0u, 0u, 0u);
+  if (4 * (4 * q + (lane >> 4)) + (PARTS > 1 ? lane & 3 : (lane >> 2) & 3) < blocks) {
+    const uint16_t* const from = src + row + (int64_t)q * 4 * kMxTile + lane * 8;
+#pragma unroll
+    for (int n = 0; n < PARTS; ++n) o.v[n] = *reinterpret_cast<const uint4*>(from + n * part);
   }
-  return v;
+  return o;
 }
 
 // P panels' products with one row (x), or the sum over slots of each slot's (h).
 // A unit is a slot's quad of K-tiles, the waves take them in turn; the next
 // unit's row and codes are loaded while the present one is multiplied, and the
-// row goes by way of LDS of the wave's own (2 KB), so that all of a unit is one
+// row goes by way of LDS of the wave's own (`mine`), so that all of a unit is one
 // trip to memory (1 token, 64 experts, 8 chosen, H = 2048, I = 1024: operands read
 // in place, tile by tile, the down product took 7.4 us instead of 4.5, the up
-// product 8.9 instead of 8.1).  `v` is the first unit's row.  fp16 x: two bf16
+// product 8.9 instead of 8.1).  Column n of the products is part n of h; the columns
+// after the last part repeat it.  `v` is the first unit's row.  fp16 x: two bf16
 // parts unless `exact`, i.e. all of the panels' weights are exact in fp16.
-template <int DT, bool PAIR, int P, int WAVES, typename RowAt, typename PanelAt>
-__device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, const uint16_t* __restrict__ src_lo,
-                                          OneRow v, RowAt&& row_at, PanelAt&& panel_at, bool exact, int slots,
-                                          const MxTiled& w, int blocks, int wave, int lane, uint4* mine,
-                                          mx_f4 (&acc)[P][1]) {
-  const int g = lane >> 4, units = slots * w.kq;
+template <int DT, int PARTS, int P, int WAVES, typename RowAt, typename PanelAt>
+__device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, int64_t part, OneRow<PARTS> v,
+                                          RowAt&& row_at, PanelAt&& panel_at, bool exact, int slots, const MxTiled& w,
+                                          int blocks, int wave, int lane, uint4* mine, mx_f4 (&acc)[P][1]) {
+  const int g = lane >> 4, column = min(lane & 15, PARTS - 1), units = slots * w.kq;
   uint4 c[P][4], next[P][4];
   uint32_t sc[P], sc_next[P];
-  OneRow v_next = v;
+  OneRow<PARTS> v_next = v;
   auto load = [&](int u, uint4 (&to)[P][4], uint32_t (&s)[P]) __attribute__((always_inline)) {
     const int q = u % w.kq;
 #pragma unroll
@@ -596,10 +629,10 @@ __device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, cons
   if (wave < units) load(wave, c, sc);
   for (int u = wave; u < units; u += WAVES) {
     const int q = u % w.kq, after = u + WAVES;
-    mine[lane] = v.hi;
-    if constexpr (PAIR) mine[64 + lane] = v.lo;
+#pragma unroll
+    for (int n = 0; n < PARTS; ++n) mine[64 * n + lane] = v.v[n];
     if (after < units) {
-      v_next = one_row<PAIR>(src, src_lo, row_at(after / w.kq), after % w.kq, blocks, lane);
+      v_next = one_row<PARTS>(src, part, row_at(after / w.kq), after % w.kq, blocks, lane);
       load(after, next, sc_next);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -608,9 +641,8 @@ __device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, cons
       if (4 * q + i >= w.kt) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = 16 * i + (PAIR ? 4 * j + g : 4 * g + j);
-        uint4 a = mine[at], b;
-        if constexpr (PAIR) b = mine[64 + at];
+        const int at = 16 * i + (PARTS > 1 ? 4 * j + g : 4 * g + j);
+        uint4 a = mine[64 * column + at], b;
         auto tile = [&](auto ct, bool two) __attribute__((always_inline)) {
           constexpr int CT = decltype(ct)::value;
 #pragma unroll
@@ -620,8 +652,7 @@ __device__ __forceinline__ void one_units(const uint16_t* __restrict__ src, cons
             if (two) acc[p][0] = mx_mfma16<CT>(d, b, acc[p][0]);
           }
         };
-        if constexpr (PAIR) tile(std::integral_constant<int, MX_BF16>{}, true);
-        else if (DT == MX_BF16 || exact) tile(std::integral_constant<int, DT>{}, false);
+        if (PARTS > 1 || DT == MX_BF16 || exact) tile(std::integral_constant<int, DT>{}, false);
         else {
           const uint4 both = a;
           mx_split8(both, a, b);
@@ -647,15 +678,14 @@ __global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint
                                                                      int renormalize, int blocks, int I,
                                                                      int32_t* __restrict__ ids,
                                                                      float* __restrict__ weights,
-                                                                     uint16_t* __restrict__ h_hi,
-                                                                     uint16_t* __restrict__ h_lo) {
-  __shared__ mx_f4 part[ONE_UP_WAVES * 2 * 64];
+                                                                     uint16_t* __restrict__ h, int64_t part) {
+  __shared__ mx_f4 sums[ONE_UP_WAVES * 2 * 64];
   __shared__ uint4 rows[ONE_UP_WAVES][64];
   __shared__ Choice choices[ONE_UP_WAVES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.z;
-  const OneRow first = one_row<false>(x, x, t * ldx, wave, blocks, lane);
+  const OneRow<1> first = one_row<1>(x, 0, t * ldx, wave, blocks, lane);
   int id;
   float mine, sum;
   choose(logits + t * E, choices[wave], E, k, renormalize != 0, lane, id, mine, sum);
@@ -663,11 +693,11 @@ __global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint
   const int64_t panel = (int64_t)expert * (2 * half) + blockIdx.x;
   const bool exact = DT == MX_BF16 || (w.flags[panel] & w.flags[panel + half] & kMxFlagF16) != 0;
   mx_f4 acc[2][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}, {mx_f4{0.f, 0.f, 0.f, 0.f}}};
-  one_units<DT, false, 2, ONE_UP_WAVES>(
-      x, x, first, [&](int) __attribute__((always_inline)) { return t * ldx; },
+  one_units<DT, 1, 2, ONE_UP_WAVES>(
+      x, 0, first, [&](int) __attribute__((always_inline)) { return t * ldx; },
       [&](int, int p) __attribute__((always_inline)) { return panel + p * half; }, exact, 1, w, blocks, wave, lane,
       rows[wave], acc);
-  share_sums<2, 1>(part, acc, wave, lane);
+  share_sums<2, 1>(sums, acc, wave, lane);
   if (wave != 0) return;
   const float weight = mine / wave_sum(sum), share = __shfl(weight, slot);
   if (blockIdx.x == 0 && slot == 0 && lane < k) {
@@ -675,34 +705,37 @@ __global__ __launch_bounds__(ONE_UP_WAVES * 64) void mx_one_up_kernel(const uint
     weights[t * k + lane] = weight;
   }
   if ((lane & 15) == 0) {
-    const mx_f4 a = total<2, 1>(part, 0, ONE_UP_WAVES, lane), b = total<2, 1>(part, 1, ONE_UP_WAVES, lane);
-    store_h(h_hi, h_lo, (t * k + slot) * h_pitch(I) + h_place(blockIdx.x * kMxPanel + 4 * (lane >> 4)), gated(a, b, share));
+    const mx_f4 a = total<2, 1>(sums, 0, ONE_UP_WAVES, lane), b = total<2, 1>(sums, 1, ONE_UP_WAVES, lane);
+    store_h(h, part, (t * k + slot) * h_pitch(I) + h_place(blockIdx.x * kMxPanel + 4 * (lane >> 4)), gated(a, b, share));
   }
 }
 
 // Workgroup: a panel of 16 columns of y, all choices of one token.
 template <int DT>
-__global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h_hi,
-                                                                         const uint16_t* __restrict__ h_lo, MxTiled w,
+__global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const uint16_t* __restrict__ h,
+                                                                         int64_t part, MxTiled w,
                                                                          const int32_t* __restrict__ ids, int k,
                                                                          int I, int H, uint16_t* __restrict__ y) {
-  __shared__ mx_f4 part[ONE_DOWN_WAVES * 64];
-  __shared__ uint4 rows[ONE_DOWN_WAVES][2 * 64];
+  __shared__ mx_f4 sums[ONE_DOWN_WAVES * 64];
+  __shared__ uint4 rows[ONE_DOWN_WAVES][3 * 64];
   const int lane = threadIdx.x & 63, blocks = I / kMxBlock;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.y;
   auto row_at = [&](int slot) __attribute__((always_inline)) { return (t * k + slot) * h_pitch(I); };
-  const OneRow first = wave < k * w.kq ? one_row<true>(h_hi, h_lo, row_at(wave / w.kq), wave % w.kq, blocks, lane)
-                                       : OneRow{};
+  const OneRow<3> first = wave < k * w.kq ? one_row<3>(h, part, row_at(wave / w.kq), wave % w.kq, blocks, lane)
+                                          : OneRow<3>{};
   mx_f4 acc[1][1] = {{mx_f4{0.f, 0.f, 0.f, 0.f}}};
-  one_units<MX_BF16, true, 1, ONE_DOWN_WAVES>(
-      h_hi, h_lo, first, row_at,
+  one_units<MX_BF16, 3, 1, ONE_DOWN_WAVES>(
+      h, part, first, row_at,
       [&](int slot, int) __attribute__((always_inline)) { return (int64_t)ids[t * k + slot] * (H / kMxPanel) + blockIdx.x; },
       true, k, w, blocks, wave, lane, rows[wave], acc);
-  share_sums<1, 1>(part, acc, wave, lane);
-  if (wave == 0 && (lane & 15) == 0)
-    *reinterpret_cast<uint2*>(y + t * H + blockIdx.x * kMxPanel + 4 * (lane >> 4)) =
-        mx_pack4<DT>(total<1, 1>(part, 0, ONE_DOWN_WAVES, lane));
+  share_sums<1, 1>(sums, acc, wave, lane);
+  if (wave == 0 && (lane & 15) == 0) {
+    mx_f4 v = total<1, 1>(sums, 0, ONE_DOWN_WAVES, lane);
+#pragma unroll
+    for (int n = 1; n < 3; ++n) v += total<1, 1>(sums, 0, ONE_DOWN_WAVES, lane + n);
+    *reinterpret_cast<uint2*>(y + t * H + blockIdx.x * kMxPanel + 4 * (lane >> 4)) = mx_pack4<DT>(v);
+  }
 }
 
 // ---------------------------------------------------------------- launches
@@ -719,26 +752,25 @@ static bool by_token(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
   return (T <= 16 && 4 * T * k <= 3 * E) || (T * H <= 12288 && T * k * H * I <= (int64_t)14 << 20);
 }
 
-static size_t h_bytes(int64_t T, int64_t I, int64_t k) { return (size_t)(T * k * h_pitch(I) * 2); }
+static int64_t h_part(int64_t T, int64_t I, int64_t k) { return T * k * h_pitch(I); }
 
-// h in two parts, then the pairs' shares of y or the tokens' logits (by_token).
+// h in three parts, then the pairs' shares of y or the tokens' logits (by_token).
 size_t mx_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t k) {
-  return 2 * h_bytes(T, I, k) + (size_t)(T * std::max<int64_t>(kMoeMaxE, k * H) * 4);
+  return (size_t)h_part(T, I, k) * 6 + (size_t)(T * std::max<int64_t>(kMoeMaxE, k * H) * 4);
 }
 
 template <int DT>
 static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renorm,
                          const void* router, const MxTiled& gate_up, const MxTiled& down, void* y, int32_t* ids,
                          float* weights, uint8_t* ws, hipStream_t stream) {
-  const int h = (int)H, i = (int)I, e = (int)E, kk = (int)k, pairs = (int)(T * k), h_blocks = h / kMxBlock;
+  const int hidden = (int)H, i = (int)I, e = (int)E, kk = (int)k, pairs = (int)(T * k), x_blocks = hidden / kMxBlock;
+  const int64_t part = h_part(T, I, k);
   auto* xp = static_cast<const uint16_t*>(x);
   auto* rp = static_cast<const uint16_t*>(router);
   auto* yp = static_cast<uint16_t*>(y);
-  auto* hi = reinterpret_cast<uint16_t*>(ws);
-  auto* lo = reinterpret_cast<uint16_t*>(ws + h_bytes(T, I, k));
-  auto* sums = reinterpret_cast<float*>(ws + 2 * h_bytes(T, I, k));
-  auto* chi = static_cast<const uint16_t*>(hi);
-  auto* clo = static_cast<const uint16_t*>(lo);
+  auto* h = reinterpret_cast<uint16_t*>(ws);
+  auto* sums = reinterpret_cast<float*>(h + 3 * part);
+  auto* ch = static_cast<const uint16_t*>(h);
   auto* cids = static_cast<const int32_t*>(ids);
   auto* cweights = static_cast<const float*>(weights);
   auto* csums = static_cast<const float*>(sums);
@@ -746,22 +778,22 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   hipError_t err;
   if (by_token(T, H, I, E, k)) {
     const unsigned t = (unsigned)T;
-    err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4), t), dim3(256), stream, xp, ldx, rp, h, e,
-                    sums);
+    err = mx_launch(mx_one_logits_kernel<DT>, dim3((unsigned)((E + 3) / 4), t), dim3(256), stream, xp, ldx, rp, hidden,
+                    e, sums);
     if (err != hipSuccess) return err;
     err = mx_launch(mx_one_up_kernel<DT>, dim3(rows, (unsigned)k, t), dim3(ONE_UP_WAVES * 64), stream, xp, ldx, gate_up,
-                    csums, e, kk, renorm, h_blocks, i, ids, weights, hi, lo);
+                    csums, e, kk, renorm, x_blocks, i, ids, weights, h, part);
     if (err != hipSuccess) return err;
-    return mx_launch(mx_one_down_kernel<DT>, dim3(panels, t), dim3(ONE_DOWN_WAVES * 64), stream, chi, clo, down, cids,
-                     kk, i, h, yp);
+    return mx_launch(mx_one_down_kernel<DT>, dim3(panels, t), dim3(ONE_DOWN_WAVES * 64), stream, ch, part, down, cids,
+                     kk, i, hidden, yp);
   }
-  err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, xp, ldx, rp, h, e, kk,
+  err = mx_launch(mx_route_kernel<DT>, dim3((unsigned)T), dim3(ROUTE_WAVES * 64), stream, xp, ldx, rp, hidden, e, kk,
                   renorm, ids, weights);
   if (err != hipSuccess) return err;
   const unsigned slots = (unsigned)std::min<int64_t>(E, pairs);
   auto up = [&](auto* kernel, unsigned q) {
     return mx_launch(kernel, dim3((rows + q - 1) / q, slots), dim3(UP_WAVES * 64), stream, xp, ldx, gate_up, cids,
-                     cweights, pairs, e, kk, h_blocks, i, hi, lo);
+                     cweights, pairs, e, kk, x_blocks, i, h, part);
   };
   // Two pairs of panels halve the loads of x, which count from about 16 rows an
   // expert (us of the layer with one and two: 32 x 2048 x 2048, 16 experts, 8 of
@@ -771,19 +803,20 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   // below (16 x 4096 x 11008, 8, 2: the product alone 77 and 111).
   err = T * k >= 16 * E ? up(mx_moe_up_kernel<DT, 2, true>, 2) : up(mx_moe_up_kernel<DT, 1, false>, 1);
   if (err != hipSuccess) return err;
-  auto go = [&](auto* kernel, unsigned p, unsigned threads) {
-    return mx_launch(kernel, dim3((panels + p - 1) / p, slots), dim3(threads), stream, chi, clo, down, cids, pairs, e, i,
-                     h, sums);
+  auto go = [&](auto* kernel, Down kind) {
+    return mx_launch(kernel, dim3((panels + DOWN_PANELS - 1) / DOWN_PANELS, slots), dim3(down_waves(kind) * 64), stream, ch,
+                     part, down, cids, pairs, e, i, hidden, sums);
   };
-  // Four panels share the loads of h.  Staged rows pay where eight waves of 256 k
-  // have work each, or where the workgroups make one round at most (us of the
-  // layer, direct and staged: 16 x 4096 x 11008, 8, 2: 136 and 129; 33 x 1056 x 736,
-  // 12, 3: 21.7 and 20.6; but 64 x 2048 x 1024, 64, 8: 92 and 102).  Two panels where
-  // four leave fewer than 1024 workgroups.
-  const unsigned quads = (panels + 3) / 4 * slots;
-  if (I >= 2048 || quads <= 256) err = go(mx_moe_down_kernel<4, true>, 4, 512);
-  else if (quads >= 1024) err = go(mx_moe_down_kernel<4, false>, 4, 256);
-  else err = go(mx_moe_down_kernel<2, false>, 2, 256);
+  // Four panels share the loads of h.  Staged rows pay where the waves have work
+  // each, or where the workgroups make one round at most; parts as rows up to five
+  // pairs an expert.  us of the product, direct, staged and few: 16 x 4096 x 11008,
+  // 8 experts, 2 chosen 52, 52 and 41.5; 40 x 4096 x 4096, 8, 1: 23.1, 22.1 and 20.5;
+  // 33 x 1056 x 736, 12, 3: 6.6, 6.4 and 9.7; 64 x 4096 x 4096, 4, 2: 38, 27.5 and 37;
+  // 64 x 2048 x 1024, 64, 8: 36, 49 and 58.
+  const bool staged = I >= 2048 || (panels + DOWN_PANELS - 1) / DOWN_PANELS * slots <= 256;
+  err = !staged ? go(mx_moe_down_kernel<Down::kDirect>, Down::kDirect)
+        : T * k <= 5 * E ? go(mx_moe_down_kernel<Down::kFew>, Down::kFew)
+                         : go(mx_moe_down_kernel<Down::kStaged>, Down::kStaged);
   if (err != hipSuccess) return err;
   const uint32_t units = (uint32_t)(H / 4);
   const int64_t n = T * units;
