@@ -56,16 +56,19 @@ __device__ __forceinline__ void gemm16_loop(const uint16_t* __restrict__ x, int6
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4, lane16 = lane * 16;
 
-  // x's rows of this tile, up to the last one's end: rows past M read as zeros.
-  const auto xb = mx_buffer(x + (int64_t)m0 * ldx, ((min(G::BM, M - m0) - 1) * ldx + (int64_t)blocks * kMxBlock) * 2);
+  // x's rows of this tile, up to the last one's end.
+  const int rows = min(G::BM, M - m0);
+  const auto xb = mx_buffer(x + (int64_t)m0 * ldx, ((rows - 1) * ldx + (int64_t)blocks * kMxBlock) * 2);
   // A piece is four rows of 256 bytes, whose 16-byte chunks are permuted (chunk
   // ^ row % 16: the reads of sixteen rows at one k then touch all banks).
-  static_assert(G::PX % 4 == 0 || G::PX < 4, "pieces four apart have the same permutation");
-  int xoff[G::PX < 4 ? G::PX : 4];
+  // xlast: in the K-tile that ends past K (`tail`, if there is one).
+  const int tail = blocks % 4 != 0 ? blocks / 4 : -1;
+  int xoff[G::PX], xlast[G::PX];
 #pragma unroll
-  for (int c = 0; c < (G::PX < 4 ? G::PX : 4); ++c) {
-    const int row = 4 * (wave * G::PX + c) + g;
-    xoff[c] = row * (int)ldx * 2 + (r ^ (row & 15)) * 16;
+  for (int c = 0; c < G::PX; ++c) {
+    const int row = 4 * (wave * G::PX + c) + g, chunk = r ^ (row & 15);
+    xoff[c] = mx_x_row(row, rows, ldx) + mx_x_chunk(chunk, 4);
+    xlast[c] = mx_x_row(row, rows, ldx) + mx_x_chunk(chunk, blocks % 4);
   }
   const auto wb = mx_buffer(w.codes + (int64_t)p0 * w.kt * 1024, (int64_t)min(G::WP, w.panels - p0) * w.kt * 1024);
   const auto sb = mx_buffer(w.scales + (int64_t)p0 * w.kq * 256, (int64_t)min(G::WP, w.panels - p0) * w.kq * 256);
@@ -76,8 +79,8 @@ __device__ __forceinline__ void gemm16_loop(const uint16_t* __restrict__ x, int6
   // A wave copies a share of the rows of x and its own panels of W.
   auto copy_x = [&](int c, int kt, uint8_t* s) __attribute__((always_inline)) {
     uint8_t* const to = s + (wave * G::PX + c) * 1024;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (__attribute__((address_space(3))) void*)to, 16, xoff[c & 3],
-                                             (c >> 2) * 16 * (int)ldx * 2 + kt * 256, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (__attribute__((address_space(3))) void*)to, 16,
+                                             kt == tail ? xlast[c] : xoff[c], kt * 256, 0, 0);
   };
   auto copy_w = [&](int c, int kt, uint8_t* s) __attribute__((always_inline)) {
     uint8_t* const to = s + (G::XP + wave * TN + c) * 1024;

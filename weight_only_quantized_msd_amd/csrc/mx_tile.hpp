@@ -63,10 +63,21 @@ __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 1" ::: "memory
 __device__ __forceinline__ void mx_keep_in_place(mx_f4& c) { asm volatile("" : "+a"(c)); }
 
 // A buffer of `bytes` (below 2^31) at a wave-uniform address: loads take their
-// address as buffer + scalar offset + lane's offset, and read 0 past its end.
+// address as buffer + scalar offset + lane's offset.  Every load stays inside it;
+// whether the limit takes the scalar offset into account is not relied on.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_buffer(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
+
+// The copies of 16-bit x: K-tile kt of a row is 256 bytes, 16 chunks of 16 bytes, and
+// a lane copies the chunk at mx_x_row + mx_x_chunk + 256 * kt from the tile's first
+// row on.  Of `rows` rows of the tile (less than 2^22 values apart) and `left` blocks
+// of the K-tile, ones past the end repeat the last row and the K-tile's first chunk:
+// their products are not stored, or zeros are multiplied instead.
+__host__ __device__ inline int mx_x_row(int row, int rows, int64_t ldx) {
+  return (row < rows ? row : rows - 1) * (int)ldx * 2;
+}
+__host__ __device__ inline int mx_x_chunk(int chunk, int left) { return chunk < 4 * left ? chunk * 16 : 0; }
 
 // fp32 partial sums: split s starts at s * M * pitch, rows are `pitch` apart, a
 // multiple of 4 so that a lane's four columns are one aligned store.
