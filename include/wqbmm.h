@@ -60,10 +60,14 @@
  *     Growth is refused while the stream is being captured into a graph:
  *     the call returns WQBMM_ERR_CAPTURE and launches nothing.  Make one
  *     eager call of the largest shape on a stream before capturing on it.
- *     Calls on different streams never share workspace.  Calls captured on a
- *     stream use that stream's workspace when their graph is replayed, so a
- *     replay must not run concurrently with other calls that use the same
- *     stream's workspace (replay on that stream, or synchronize in between).
+ *     Calls on different streams never share workspace.  Host threads may call
+ *     on one stream at the same time: the launches of a call that uses the
+ *     workspace are made together, before or after another's.  On
+ *     hipStreamPerThread each thread has a workspace, kept when it ends.
+ *     Calls captured on a stream use that stream's workspace when their graph
+ *     is replayed, so a replay must not run concurrently with other calls that
+ *     use the same stream's workspace (replay on that stream, or synchronize
+ *     in between).
  *   - Results are deterministic: the same inputs give bit-identical outputs.
  *   - Only gfx950 (MI355X) is supported: other devices give WQBMM_ERR_UNSUPPORTED.
  *   - Finite inputs are assumed; Inf/NaN inputs give unspecified outputs.

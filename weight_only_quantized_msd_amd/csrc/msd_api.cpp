@@ -13,11 +13,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 #include <vector>
 
 #include "../../include/wqbmm.h"
@@ -131,7 +132,7 @@ bool capturing(hipStream_t stream, wqbmm_status* err) {
   return cs != hipStreamCaptureStatusNone;
 }
 
-// ---- per-(device, stream) workspace of wqbmm_a16w4_msd and friends
+// ---- per-(device, stream) workspace of wqbmm_a16w4_msd, wqbmm_mxfp4_matmul and friends
 // Grown on demand, never while the stream is being captured (a captured graph
 // would hold the growth's allocation and zeroing only inside the graph), and
 // never freed: a buffer that a larger one replaces is retired but stays
@@ -141,7 +142,12 @@ bool capturing(hipStream_t stream, wqbmm_status* err) {
 // of a stream add up to less than its current one.  The accumulator region
 // of a new buffer is zeroed by a kernel on the stream, ahead of the call's
 // own kernels; nothing synchronizes the host.
+//
+// A call passes operands between its launches in the workspace, so it holds `mu`
+// from the lookup to its last launch: calls of other host threads on the same stream
+// launch before or after, never in between.
 struct Workspace {
+  std::mutex mu;
   void* base = nullptr;
   size_t acc_bytes = 0;
   size_t ops_bytes = 0;
@@ -151,21 +157,42 @@ struct Workspace {
   int64_t prep_gs = 0, prep_m = -1, prep_k = 0, prep_n = 0;
   bool prep_opw = false;
 };
-std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
+std::map<std::tuple<int, hipStream_t, uint64_t>, Workspace> g_ws;   // the map and g_retired: under g_mu
 std::vector<void*> g_retired;
+
+// hipStreamPerThread is one handle for a stream of each thread's own: a number of the
+// calling thread's (never used again) tells their workspaces apart.
+uint64_t thread_of(hipStream_t stream) {
+  if (stream != hipStreamPerThread) return 0;
+  static std::atomic<uint64_t> last{0};
+  static thread_local const uint64_t mine = ++last;
+  return mine;
+}
+
+void retire(void* p) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  g_retired.push_back(p);
+}
 
 size_t grown(size_t have, size_t need) {
   if (need <= have) return have;
   return std::max(need + need / 4, 2 * have);
 }
 
-wqbmm_status get_workspace(int dev, hipStream_t stream, const Needs& need, Buffers* out) {
-  if (need.acc == 0 && need.ops == 0) {   // e.g. the fused decode kernel without a K split
-    *out = Buffers{};
-    return WQBMM_OK;
+// The stream's workspace, with at least `need`; *held keeps it this call's until the
+// call has made its launches.  Nothing needed: *ws is null and nothing is held.
+wqbmm_status get_workspace(int dev, hipStream_t stream, const Needs& need, Buffers* out, Workspace** ws_out,
+                           std::unique_lock<std::mutex>* held) noexcept try {
+  *out = Buffers{};
+  *ws_out = nullptr;
+  if (need.acc == 0 && need.ops == 0) return WQBMM_OK;   // e.g. the fused decode kernel without a K split
+  Workspace* found;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    found = &g_ws[std::make_tuple(dev, stream, thread_of(stream))];
   }
-  std::lock_guard<std::mutex> lk(g_mu);
-  Workspace& ws = g_ws[std::make_pair(dev, stream)];
+  Workspace& ws = *found;
+  *held = std::unique_lock<std::mutex>(ws.mu);
   if (!ws.base || ws.acc_bytes < need.acc || ws.ops_bytes < need.ops) {
     wqbmm_status st;
     if (capturing(stream, &st)) return WQBMM_ERR_CAPTURE;
@@ -175,10 +202,10 @@ wqbmm_status get_workspace(int dev, hipStream_t stream, const Needs& need, Buffe
     void* p = nullptr;
     if (hipMalloc(&p, acc + ops + 256) != hipSuccess) return WQBMM_ERR_ALLOC;
     if (wqbmm::launch_zero_words(static_cast<uint32_t*>(p), (int64_t)(acc / 4), stream) != hipSuccess) {
-      g_retired.push_back(p);
+      retire(p);
       return WQBMM_ERR_LAUNCH;
     }
-    if (ws.base) g_retired.push_back(ws.base);
+    if (ws.base) retire(ws.base);
     ws.base = p;
     ws.acc_bytes = acc;
     ws.ops_bytes = ops;
@@ -188,7 +215,10 @@ wqbmm_status get_workspace(int dev, hipStream_t stream, const Needs& need, Buffe
   out->acc_bytes = ws.acc_bytes;
   out->ops = static_cast<uint8_t*>(ws.base) + ws.acc_bytes;
   out->ops_bytes = ws.ops_bytes;
+  *ws_out = found;
   return WQBMM_OK;
+} catch (...) {
+  return WQBMM_ERR_ALLOC;
 }
 
 }  // namespace
@@ -198,21 +228,17 @@ namespace wqbmm {
 
 wqbmm_status host_check_device(int* dev_out) noexcept { return check_device(dev_out); }
 
-wqbmm_status host_workspace(int dev, hipStream_t stream, size_t bytes, uint8_t** ws) noexcept {
+wqbmm_status host_workspace(int dev, hipStream_t stream, size_t bytes, uint8_t** ws,
+                            std::unique_lock<std::mutex>* held) noexcept {
   *ws = nullptr;
-  if (bytes == 0) return WQBMM_OK;
-  try {
-    Needs need;
-    need.ops = round_up(bytes, 256);
-    Buffers b;
-    const wqbmm_status st = get_workspace(dev, stream, need, &b);
-    if (st != WQBMM_OK) return st;
-    *ws = b.ops;
-    std::lock_guard<std::mutex> lk(g_mu);
-    g_ws[std::make_pair(dev, stream)].prep_path = 0;   // the call overwrites prepared operands
-  } catch (...) {
-    return WQBMM_ERR_ALLOC;
-  }
+  Needs need;
+  need.ops = round_up(bytes, 256);
+  Buffers b;
+  Workspace* found = nullptr;
+  const wqbmm_status st = get_workspace(dev, stream, need, &b, &found, held);
+  if (st != WQBMM_OK || !found) return st;
+  found->prep_path = 0;                                  // the call overwrites prepared operands
+  *ws = b.ops;
   return WQBMM_OK;
 }
 
@@ -268,12 +294,10 @@ int resolve_path(int path, int64_t M, int64_t K, int64_t N, int64_t gs) {
 wqbmm_status launch_status(hipError_t e) { return e == hipSuccess ? WQBMM_OK : WQBMM_ERR_LAUNCH; }
 
 // Records (stage 0 or 1) or checks (stage 2) which path and shape the
-// operands in the ops region of (dev, stream) belong to, and whether the
-// weights' operand form stood in for the weight tiles.
-wqbmm_status track_operands(int dev, hipStream_t stream, int path, int stage, int64_t gs, int64_t M,
-                            int64_t K, int64_t N, bool opw) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  Workspace& ws = g_ws[std::make_pair(dev, stream)];
+// operands in the workspace's ops region belong to, and whether the weights'
+// operand form stood in for the weight tiles.
+wqbmm_status track_operands(Workspace& ws, int path, int stage, int64_t gs, int64_t M, int64_t K, int64_t N,
+                            bool opw) {
   if (stage == 2)
     return (ws.prep_path == path && ws.prep_gs == gs && ws.prep_m == M && ws.prep_k == K &&
             ws.prep_n == N && ws.prep_opw == opw)
@@ -341,11 +365,13 @@ wqbmm_status run(const void* x, const void* w, const void* w_op, const void* sca
   if (st != WQBMM_OK) return st;
   const bool opw = uses_operand_weights(path, gs, w_op);
   Buffers b;
-  st = get_workspace(dev, stream, needs_of(path, gs, M, K, N, g_begin, g_end, y_int != nullptr, opw), &b);
+  Workspace* ws = nullptr;
+  std::unique_lock<std::mutex> held;
+  st = get_workspace(dev, stream, needs_of(path, gs, M, K, N, g_begin, g_end, y_int != nullptr, opw), &b, &ws, &held);
   if (st != WQBMM_OK) return st;
   const bool two_kernels = path == WQBMM_PATH_PREFILL || M > 4;
-  if (two_kernels) {
-    st = track_operands(dev, stream, path, stage, gs, M, K, N, opw);
+  if (two_kernels && ws) {
+    st = track_operands(*ws, path, stage, gs, M, K, N, opw);
     if (st != WQBMM_OK) return st;
   }
   return run_path(b, path, x, w, w_op, scale, gs, M, K, N, g_begin, g_end, y, y_int, stage, stream);

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/wqbmm_mxfp4.h"
 #include "mx_launch.hpp"
@@ -96,7 +97,8 @@ wqbmm_status wqbmm_mxfp4_matmul(const void* x, int dtype, int64_t ldx, const voi
   }
   const MxGemmPlan plan = act ? mx_gemm4_plan(M, K, N) : mx_gemm16_plan(M, K, N);
   uint8_t* ws = nullptr;
-  st = host_workspace(dev, s, plan.x_bytes + plan.part_bytes, &ws);
+  std::unique_lock<std::mutex> held;
+  st = host_workspace(dev, s, plan.x_bytes + plan.part_bytes, &ws, &held);
   if (st != WQBMM_OK) return st;
   return status_of(act ? launch_mx_gemm4(x, dtype, ldx, w, M, K, N, y, plan, ws, s)
                        : launch_mx_gemm16(x, dtype, ldx, w, M, K, N, y, plan, ws, s));
@@ -119,7 +121,8 @@ wqbmm_status wqbmm_mxfp4_moe(const void* x, int dtype, int64_t ldx, int64_t T, i
   if (st != WQBMM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = nullptr;
-  st = host_workspace(dev, s, mx_moe_workspace_bytes(T, H, I, k), &ws);
+  std::unique_lock<std::mutex> held;
+  st = host_workspace(dev, s, mx_moe_workspace_bytes(T, H, I, k), &ws, &held);
   if (st != WQBMM_OK) return st;
   return status_of(launch_mx_moe(x, dtype, ldx, T, H, I, E, k, renormalize != 0, router, mx_view(gate_up, H, E * 2 * I),
                                  mx_view(down, I, E * H), y, topk_ids, topk_weights, ws, s));

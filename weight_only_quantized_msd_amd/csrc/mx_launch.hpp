@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "../../include/wqbmm.h"
@@ -116,9 +117,11 @@ hipError_t launch_mx_moe(const void* x, int dtype, int64_t ldx, int64_t T, int64
                          hipStream_t stream);
 
 // Host services of msd_api.cpp: the device check (*dev_out: the current
-// device), and `bytes` of the stream's workspace (wqbmm.h's rules).  They
-// throw nothing.
+// device), and `bytes` of the stream's workspace (wqbmm.h's rules), the caller's
+// until *held goes: it is kept until the call has made its last launch.  They throw
+// nothing.
 wqbmm_status host_check_device(int* dev_out) noexcept;
-wqbmm_status host_workspace(int dev, hipStream_t stream, size_t bytes, uint8_t** ws) noexcept;
+wqbmm_status host_workspace(int dev, hipStream_t stream, size_t bytes, uint8_t** ws,
+                            std::unique_lock<std::mutex>* held) noexcept;
 
 }  // namespace wqbmm
