@@ -24,6 +24,10 @@
  *   - ld* is the distance between rows in elements: at least the row length
  *     and a multiple of 8; every pointer is 16-byte aligned.
  *   - Infinities and NaN are followed: they give what the formulas give.
+ *   - Weights of 2^128 and more (4 and 6 at scale 253, 2 and more at 254: fp32
+ *     does not hold them either, and wqbmm_mxfp4_quantize makes none) are
+ *     beyond the products with 16-bit x and the expert layer: what they are
+ *     multiplied into comes out infinite or NaN, as if they were infinite.
  */
 #ifndef WQBMM_MXFP4_H
 #define WQBMM_MXFP4_H
@@ -76,7 +80,7 @@ wqbmm_status wqbmm_mxfp4_tile_weights(const void* codes, const void* scales, int
 
 /*
  * y [M][N] = x [M][K] . W^T, F16 or BF16, sums in fp32, rounded once.
- * act = WQBMM_MXFP4_ACT_16BIT: the products x*w are exact.
+ * act = WQBMM_MXFP4_ACT_16BIT: the products x*w are exact (|w| < 2^128).
  * act = WQBMM_MXFP4_ACT_MXFP4: x is first quantised to MXFP4.
  */
 wqbmm_status wqbmm_mxfp4_matmul(const void* x, int dtype, int64_t ldx, const void* w_tiled,

@@ -8,7 +8,8 @@
 //   * 16-bit x: the chunk's four dwords convert to four operands of
 //     v_mfma_f32_16x16x32 (8 consecutive k of each of four blocks per
 //     instruction; both operands use the same k), the block's scale applied by
-//     the conversion, which is exact in bf16 for every scale;
+//     the conversion, which is exact in bf16 below 2^128 (beyond, at scales 253
+//     and 254, it gives infinities);
 //   * MXFP4 x: the lane holds the whole block l/16 of x's row l%16 as well, so
 //     it quantises it in registers (no preparation kernel), and the chunk is
 //     the scaled MFMA's operand as it is.
