@@ -57,9 +57,13 @@ REPLAYS = 11                 # extra timed replays of the K-step graph for media
 
 
 def kernel_sources_sha() -> str:
+    """Of the files that the workloads' kernels come from (msd_*.hip and their
+    headers); other operators' sources and host code do not change them."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "weight_only_quantized_msd_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
+        if not (f.startswith("msd_") and f.endswith((".hip", ".hpp"))):
+            continue
         h.update(f.encode())
         h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
