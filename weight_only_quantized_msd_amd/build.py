@@ -69,12 +69,13 @@ def build(verbose: bool = False) -> str:
 
 def build_calls(verbose: bool = False) -> str:
     """_mx_calls.so: the Python module of csrc/mx_torch.cpp (host code, linked to
-    torch and to libwqbmm.so beside it, which build() must have made)."""
+    torch and to libwqbmm.so beside it, which build() must have made).  It needs
+    g++ and torch with its headers; the C library needs neither."""
     import sysconfig
     from torch.utils.cpp_extension import include_paths, library_paths
     dirs = include_paths() + [os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
                               sysconfig.get_paths()["include"]]
-    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM"]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM"]
            + [a for d in dirs for a in ("-isystem", d)] + [os.path.join(CSRC, "mx_torch.cpp"), "-o", CALLS_PATH + ".tmp"]
            + [f"-L{_HERE}", "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
            + [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"])
