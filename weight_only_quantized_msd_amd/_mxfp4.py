@@ -7,6 +7,9 @@ outputs on the current stream of the current device, is made in C++
 (csrc/mx_torch.cpp, the module _mx_calls); what that hands back undone takes the
 way below, which also says what is wrong with a call.
 
+The calls have no gradients.  What they return for inputs that require one carries
+the call in its history, and a backward pass that reaches it raises.
+
 Format: 32 consecutive values along the last dimension share a scale byte s
 that stands for 2^(s - 127) (255: NaN); two 4-bit elements to a byte, the lower
 index in the low nibble.
@@ -19,12 +22,13 @@ from ._lib import WQBMM_ERR_INVALID, check, lib
 _ACTS = {"16bit": _lib.WQBMM_MXFP4_ACT_16BIT, "mxfp4": _lib.WQBMM_MXFP4_ACT_MXFP4}
 _torch = None            # torch and what is looked up in it once, set by _load
 _calls = None            # csrc/mx_torch.cpp
+_end_of_history = None   # an autograd function without a backward pass
 _dtypes = {}
 _device_now = _raw_stream = None
 
 
 def _load():
-    global _torch, _device_now, _raw_stream, _calls
+    global _torch, _device_now, _raw_stream, _calls, _end_of_history
     import torch
     lib()
     try:
@@ -35,7 +39,34 @@ def _load():
                     torch.float32: _lib.WQBMM_DTYPE_F32})
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _torch, _calls = torch, _mx_calls
+
+    class EndOfHistory(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, where, outputs, *inputs):
+            ctx.where = where
+            ctx.mark_non_differentiable(*[t for t in outputs if not t.is_floating_point()])
+            return tuple(outputs)
+
+        @staticmethod
+        def backward(ctx, *gradients):
+            raise RuntimeError(f"{ctx.where} has no gradient")
+
+    _end_of_history = EndOfHistory
     return torch
+
+
+def _needs_gradient(*inputs):
+    return _torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+
+
+def _refuse_given_output(y, where, *inputs):
+    if y is not None and _needs_gradient(y, *inputs):
+        raise RuntimeError(f"{where} has no gradient: with y given, its inputs and y must not require one")
+
+
+def _with_history(where, outputs, *inputs):
+    """outputs, with a history that ends in an error if an input requires a gradient."""
+    return _end_of_history.apply(where, outputs, *inputs) if _needs_gradient(*inputs) else outputs
 
 
 def _dtype_code(dtype, allow_fp32):
@@ -193,6 +224,7 @@ def wqbmm_mxfp4_matmul(x, w_tiled, N: int, activations: str = "16bit", y=None, s
     code = _dtype_code(x.dtype, False)
     device = x.device
     _check_tiled(w_tiled, K, N, "w_tiled", device)
+    _refuse_given_output(y, "wqbmm_mxfp4_matmul", x)
     if y is not None:
         _exactly(y, (M, N), x.dtype, "y", device)
 
@@ -202,7 +234,7 @@ def wqbmm_mxfp4_matmul(x, w_tiled, N: int, activations: str = "16bit", y=None, s
               "wqbmm_mxfp4_matmul")
         return out
 
-    return _on(device, stream, work)
+    return _with_history("wqbmm_mxfp4_matmul", (_on(device, stream, work),), x)[0]
 
 
 def wqbmm_mxfp4_moe(x, router, gate_up, down, intermediate: int, top_k: int, renormalize: bool = True, y=None,
@@ -229,6 +261,7 @@ def wqbmm_mxfp4_moe(x, router, gate_up, down, intermediate: int, top_k: int, ren
     _exactly(router, (E, H), x.dtype, "router", device)
     _check_tiled(gate_up, H, E * 2 * intermediate, "gate_up", device)
     _check_tiled(down, intermediate, E * H, "down", device)
+    _refuse_given_output(y, "wqbmm_mxfp4_moe", x, router)
     if y is not None:
         _exactly(y, (T, H), x.dtype, "y", device)
 
@@ -242,4 +275,4 @@ def wqbmm_mxfp4_moe(x, router, gate_up, down, intermediate: int, top_k: int, ren
               "wqbmm_mxfp4_moe")
         return out, ids, weights
 
-    return _on(device, stream, work)
+    return _with_history("wqbmm_mxfp4_moe", _on(device, stream, work), x, router)

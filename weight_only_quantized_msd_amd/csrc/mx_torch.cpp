@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -45,6 +46,9 @@ bool rows_of(const at::Tensor& t, int64_t* ld) {
 bool is_bytes(const at::Tensor& t, int64_t numel) {
   return t.scalar_type() == at::kByte && on_current_device(t) && t.is_contiguous() && t.numel() == numel;
 }
+
+// The other way ends the outputs' history in an error.
+bool needs_gradient(const at::Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
 
 void* stream_of(const at::Tensor& t) { return c10::hip::getCurrentHIPStream(t.get_device()).stream(); }
 
@@ -99,7 +103,7 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor* x = n == 4 ? tensor(args[0]) : nullptr;
   const at::Tensor* w = n == 4 ? tensor(args[1]) : nullptr;
   int64_t ld;
-  if (!x || !w || !rows_of(*x, &ld) || !PyLong_Check(args[2])) return other_way();
+  if (!x || !w || !rows_of(*x, &ld) || !PyLong_Check(args[2]) || needs_gradient(*x)) return other_way();
   const int code = dtype_code(x->scalar_type());
   const long long N = PyLong_AsLongLong(args[2]);
   const long act = PyLong_AsLong(args[3]);
@@ -125,7 +129,8 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
     down = tensor(args[3]);
   }
   int64_t ld;
-  if (!x || !router || !gate_up || !down || !rows_of(*x, &ld) || !PyLong_Check(args[4]) || !PyLong_Check(args[5]))
+  if (!x || !router || !gate_up || !down || !rows_of(*x, &ld) || !PyLong_Check(args[4]) || !PyLong_Check(args[5]) ||
+      needs_gradient(*x) || needs_gradient(*router))
     return other_way();
   const int code = dtype_code(x->scalar_type());
   const long long I = PyLong_AsLongLong(args[4]), k = PyLong_AsLongLong(args[5]);
