@@ -104,6 +104,8 @@ def _on(device, stream, work):
             return work(_raw_stream(device.index))
         with _torch.cuda.device(device):
             return work(_raw_stream(device.index))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with _torch.cuda.stream(stream):
         return work(stream.cuda_stream)
 
