@@ -27,14 +27,23 @@ _dtypes = {}
 _device_now = _raw_stream = None
 
 
+class _TheOtherWay:
+    """_mx_calls that hands every call back."""
+    quantize = dequantize = matmul = moe = staticmethod(lambda *args: None)
+
+
 def _load():
     global _torch, _device_now, _raw_stream, _calls, _end_of_history
     import torch
     lib()
-    try:
-        from . import _mx_calls
-    except ImportError as e:
-        raise RuntimeError("_mx_calls.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'`") from e
+    if _lib.OTHER_LIB:                      # _mx_calls would load the package's own beside it
+        _mx_calls = _TheOtherWay
+    else:
+        try:
+            from . import _mx_calls
+        except ImportError as e:
+            raise RuntimeError("_mx_calls.so is not built; "
+                               "run `python -c 'import __graft_entry__ as g; g.build()'`") from e
     _dtypes.update({torch.float16: _lib.WQBMM_DTYPE_F16, torch.bfloat16: _lib.WQBMM_DTYPE_BF16,
                     torch.float32: _lib.WQBMM_DTYPE_F32})
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
