@@ -250,7 +250,7 @@ __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int p
 //     whole rows a copy, the 16-byte chunks of a row permuted (chunk ^ row % 16);
 //   direct: each lane loads its 16-byte operands, which touches a cache line a
 //     lane, but needs no LDS, so more workgroups share a CU.
-// Staged is for experts with more than a few rows (moe_dt's rules).
+// moe_dt says which.
 enum class Rows {
   kAsIs,       // 16-bit
   kSplit,      // fp16 as two bf16
@@ -743,10 +743,10 @@ __global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const 
 // four.  By itself every pair reads its expert's weights, which pays while most
 // pairs have experts of their own (T * k <= 3/4 E), or while all that reading is
 // small and the workgroups are few.  us of the layer together and by token (T, H,
-// I, E, k): 2 x 2048 x 1024, 64, 8 28.9 and 18.9; 6: 52.0 and 42.7; 12: 64.6 and
-// 68.2; 16 x 4096 x 1024, 256, 8 211 and 182; 3 x 4096 x 4096, 16, 4 69.5 and 70.9,
-// 4: 78.1 and 86.7; 6 x 1056 x 736, 12, 3 17.7 and 16.5, 8: 18.3 and 20.1; 24 x 512 x
-// 256, 4, 1 13.8 and 13.0, 32: 14.1 and 14.3; 24 x 1024 x 256, 64, 1 15.9 and 18.5.
+// I, E, k): 2 x 2048 x 1024, 64, 8 26.3 and 18.5; 6: 50.6 and 41.0; 12: 63.8 and
+// 66.8; 16 x 4096 x 1024, 256, 8 207 and 177; 3 x 4096 x 4096, 16, 4 75.1 and 69.2,
+// 4: 83.9 and 84.2; 6 x 1056 x 736, 12, 3 18.1 and 16.2, 8: 18.6 and 19.7; 24 x 512 x
+// 256, 4, 1 14.0 and 12.8, 32: 14.2 and 14.1; 24 x 1024 x 256, 64, 1 17.6 and 18.5.
 static bool by_token(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
   if (T == 1) return true;
   return (T <= 16 && 4 * T * k <= 3 * E) || (T * H <= 12288 && T * k * H * I <= (int64_t)14 << 20);
@@ -795,13 +795,14 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
     return mx_launch(kernel, dim3((rows + q - 1) / q, slots), dim3(UP_WAVES * 64), stream, xp, ldx, gate_up, cids,
                      cweights, pairs, e, kk, x_blocks, i, h, part);
   };
-  // Two pairs of panels halve the loads of x, which count from about 16 rows an
-  // expert (us of the layer with one and two: 32 x 2048 x 2048, 16 experts, 8 of
-  // them chosen 57 and 52; 33 x 1056 x 736, 12, 3: 20.9 and 21.6); staged rows then
-  // pay too (direct and staged: 64 x 4096 x 4096, 4, 2: 63.5 and 59.4; 48 x 2048 x
-  // 1024, 16, 8: 49.9 and 47.6; 64 x 1056 x 736, 12, 3: 23.4 and 23.9), but not
-  // below (16 x 4096 x 11008, 8, 2: the product alone 77 and 111).
-  err = T * k >= 16 * E ? up(mx_moe_up_kernel<DT, 2, true>, 2) : up(mx_moe_up_kernel<DT, 1, false>, 1);
+  // Two pairs of panels share staged rows where each wave has a unit of four K-tiles
+  // (H >= 2048), or where many rows make up for fewer; else direct rows, a pair.  us
+  // of the layer, direct and staged: 16 x 4096 x 11008, 8 experts, 2 chosen 131.9 and
+  // 126.2; 48 x 2048 x 1024, 16, 8: 47.0 and 40.4; 64 x 2048 x 1024, 64, 8: 93.9 and
+  // 92.0; 64 x 1024 x 4096, 4, 2: 46.2 and 43.2; but 64 x 1056 x 736, 12, 3: 24.3 and
+  // 24.9; 33 x 1056 x 736, 12, 3: 20.5 and 21.4; 64 x 256 x 256, 4, 2: 19.6 and 22.0.
+  const bool staged_x = H >= 2048 || (H >= 512 && T * k >= 24 * E);
+  err = staged_x ? up(mx_moe_up_kernel<DT, 2, true>, 2) : up(mx_moe_up_kernel<DT, 1, false>, 1);
   if (err != hipSuccess) return err;
   auto go = [&](auto* kernel, Down kind) {
     return mx_launch(kernel, dim3((panels + DOWN_PANELS - 1) / DOWN_PANELS, slots), dim3(down_waves(kind) * 64), stream, ch,
@@ -813,8 +814,8 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   // 8 experts, 2 chosen 52, 52 and 41.5; 40 x 4096 x 4096, 8, 1: 23.1, 22.1 and 20.5;
   // 33 x 1056 x 736, 12, 3: 6.6, 6.4 and 9.7; 64 x 4096 x 4096, 4, 2: 38, 27.5 and 37;
   // 64 x 2048 x 1024, 64, 8: 36, 49 and 58.
-  const bool staged = I >= 2048 || (panels + DOWN_PANELS - 1) / DOWN_PANELS * slots <= 256;
-  err = !staged ? go(mx_moe_down_kernel<Down::kDirect>, Down::kDirect)
+  const bool staged_h = I >= 2048 || (panels + DOWN_PANELS - 1) / DOWN_PANELS * slots <= 256;
+  err = !staged_h ? go(mx_moe_down_kernel<Down::kDirect>, Down::kDirect)
         : T * k <= 5 * E ? go(mx_moe_down_kernel<Down::kFew>, Down::kFew)
                          : go(mx_moe_down_kernel<Down::kStaged>, Down::kStaged);
   if (err != hipSuccess) return err;
