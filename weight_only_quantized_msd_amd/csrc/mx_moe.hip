@@ -13,12 +13,12 @@
 // itself from the ids (at most 1024 of them).
 //
 // Bound by the weights: 16 tokens, H = 4096, I = 11008, 8 experts, 2 chosen: route
-// 6 us, up 76 (383 MB, 5.0 TB/s), down 40 (191 MB, 4.8 TB/s), sum 4.  Small layers
+// 6 us, up 73 (383 MB, 5.2 TB/s), down 41 (191 MB, 4.7 TB/s), sum 4.  Small layers
 // are bound by the chain of launches and trips to memory: 33 tokens, H = 1056, I =
-// 736, 12 experts, 3 chosen: 4.5 + 7.5 + 5.1 + 2.4 us.
+// 736, 12 experts, 3 chosen: 4.6 + 7.9 + 6.2 + 2.5 us.
 //
 // One token, and few, are taken by themselves in three launches, at the end of
-// this file: 1 token, H = 2048, I = 1024, 64 experts, 8 chosen: 2.6 + 8.2 + 4.4 us.
+// this file: 1 token, H = 2048, I = 1024, 64 experts, 8 chosen: 2.8 + 7.9 + 5.6 us.
 #include <algorithm>
 
 #include "mx_tile.hpp"
@@ -246,7 +246,7 @@ __device__ __forceinline__ int slot_pairs(const int32_t* __restrict__ ids, int p
 // Both products of an expert are the same contraction: P panels of its weights
 // with the rows of its pairs (tokens' x; h), the waves of a workgroup taking
 // units of U K-tiles in turn.  The rows come in one of two ways:
-//   staged: each wave copies a unit's rows to 16 KB of LDS of its own, 1 KB of
+//   staged: each wave copies a unit's rows to LDS of its own (8 to 24 KB), 1 KB of
 //     whole rows a copy, the 16-byte chunks of a row permuted (chunk ^ row % 16);
 //   direct: each lane loads its 16-byte operands, which touches a cache line a
 //     lane, but needs no LDS, so more workgroups share a CU.
