@@ -603,8 +603,8 @@ __device__ __forceinline__ OneRow<PARTS> one_row(const uint16_t* __restrict__ sr
 // unit's row and codes are loaded while the present one is multiplied, and the
 // row goes by way of LDS of the wave's own (`mine`), so that all of a unit is one
 // trip to memory (1 token, 64 experts, 8 chosen, H = 2048, I = 1024: operands read
-// in place, tile by tile, the down product took 7.4 us instead of 4.5, the up
-// product 8.9 instead of 8.1).  Column n of the products is part n of h; the columns
+// in place, tile by tile, the down product took 7.4 us instead of 4.5 with h in two
+// parts, the up product 8.9 instead of 8.1).  Column n of the products is part n of h; the columns
 // after the last part repeat it.  `v` is the first unit's row.  fp16 x: two bf16
 // parts unless `exact`, i.e. all of the panels' weights are exact in fp16.
 template <int DT, int PARTS, int P, int WAVES, typename RowAt, typename PanelAt>
@@ -730,12 +730,13 @@ __global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const 
       [&](int slot, int) __attribute__((always_inline)) { return (int64_t)ids[t * k + slot] * (H / kMxPanel) + blockIdx.x; },
       true, k, w, blocks, wave, lane, rows[wave], acc);
   share_sums<1, 1>(sums, acc, wave, lane);
-  if (wave == 0 && (lane & 15) == 0) {
-    mx_f4 v = total<1, 1>(sums, 0, ONE_DOWN_WAVES, lane);
+  if (wave != 0) return;
+  const mx_f4 mine = total<1, 1>(sums, 0, ONE_DOWN_WAVES, lane);        // of part lane % 16
+  mx_f4 v;
 #pragma unroll
-    for (int n = 1; n < 3; ++n) v += total<1, 1>(sums, 0, ONE_DOWN_WAVES, lane + n);
+  for (int i = 0; i < 4; ++i) v[i] = mine[i] + __shfl_down(mine[i], 1) + __shfl_down(mine[i], 2);
+  if ((lane & 15) == 0)
     *reinterpret_cast<uint2*>(y + t * H + blockIdx.x * kMxPanel + 4 * (lane >> 4)) = mx_pack4<DT>(v);
-  }
 }
 
 // ---------------------------------------------------------------- launches
