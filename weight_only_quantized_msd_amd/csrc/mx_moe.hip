@@ -15,10 +15,10 @@
 // Bound by the weights: 16 tokens, H = 4096, I = 11008, 8 experts, 2 chosen: route
 // 6 us, up 73 (383 MB, 5.2 TB/s), down 41 (191 MB, 4.7 TB/s), sum 4.  Small layers
 // are bound by the chain of launches and trips to memory: 33 tokens, H = 1056, I =
-// 736, 12 experts, 3 chosen: 4.6 + 7.9 + 6.2 + 2.5 us.
+// 736, 12 experts, 3 chosen: 4.6 + 7.9 + 5.8 + 2.5 us.
 //
 // One token, and few, are taken by themselves in three launches, at the end of
-// this file: 1 token, H = 2048, I = 1024, 64 experts, 8 chosen: 2.8 + 7.9 + 5.6 us.
+// this file: 1 token, H = 2048, I = 1024, 64 experts, 8 chosen: 2.8 + 8.1 + 5.1 us.
 #include <algorithm>
 
 #include "mx_tile.hpp"
@@ -297,7 +297,7 @@ __device__ __forceinline__ void expert_units(const uint16_t* __restrict__ src, i
                                              int wave, int waves, int lane, uint8_t* xs, mx_f4 (&acc)[P][MT]) {
   constexpr bool H = MODE == Rows::kParts || MODE == Rows::kPartRows;
   constexpr int PARTS = MODE == Rows::kParts ? 3 : 1, TERMS = MODE == Rows::kSplit ? 2 : PARTS;
-  constexpr int U = !H ? (STAGED ? 4 / MT : 4) : STAGED ? 2 / MT : 2;
+  constexpr int U = !H ? (STAGED ? 4 / MT : 4) : !STAGED ? 2 : PARTS > 1 ? 1 : 2 / MT;
   constexpr int LANES = 16 * U, ROWS = 64 / LANES;
   constexpr int CT = MODE == Rows::kAsIs ? DT : MX_BF16;
   const int r = lane & 15, g = lane >> 4;
@@ -744,7 +744,7 @@ __global__ __launch_bounds__(ONE_DOWN_WAVES * 64) void mx_one_down_kernel(const 
 // four.  By itself every pair reads its expert's weights, which pays while most
 // pairs have experts of their own (T * k <= 3/4 E), or while all that reading is
 // small and the workgroups are few.  us of the layer together and by token (T, H,
-// I, E, k): 2 x 2048 x 1024, 64, 8 26.3 and 18.5; 6: 50.6 and 41.0; 12: 63.8 and
+// I, E, k): 2 x 2048 x 1024, 64, 8 26.3 and 18.1; 6: 50.6 and 41.0; 12: 63.8 and
 // 66.8; 16 x 4096 x 1024, 256, 8 207 and 177; 3 x 4096 x 4096, 16, 4 75.1 and 69.2,
 // 4: 83.9 and 84.2; 6 x 1056 x 736, 12, 3 18.1 and 16.2, 8: 18.6 and 19.7; 24 x 512 x
 // 256, 4, 1 14.0 and 12.8, 32: 14.2 and 14.1; 24 x 1024 x 256, 64, 1 17.6 and 18.5.
@@ -813,7 +813,7 @@ static hipError_t moe_dt(const void* x, int64_t ldx, int64_t T, int64_t H, int64
   // each, or where the workgroups make one round at most; parts as rows up to five
   // pairs an expert.  us of the product, direct, staged and few: 16 x 4096 x 11008,
   // 8 experts, 2 chosen 52, 52 and 41.5; 40 x 4096 x 4096, 8, 1: 23.1, 22.1 and 20.5;
-  // 33 x 1056 x 736, 12, 3: 6.6, 6.4 and 9.7; 64 x 4096 x 4096, 4, 2: 38, 27.5 and 37;
+  // 33 x 1056 x 736, 12, 3: 6.6, 5.8 and 9.7; 64 x 4096 x 4096, 4, 2: 38, 27.5 and 37;
   // 64 x 2048 x 1024, 64, 8: 36, 49 and 58.
   const bool staged_h = I >= 2048 || (panels + DOWN_PANELS - 1) / DOWN_PANELS * slots <= 256;
   err = !staged_h ? go(mx_moe_down_kernel<Down::kDirect>, Down::kDirect)
