@@ -27,6 +27,10 @@ constexpr int MX_F16 = 0, MX_BF16 = 1, MX_F32 = 2;     // wqbmm_dtype
 
 __device__ __forceinline__ float mx_scale(uint32_t s) { return __uint_as_float(s << 23); }
 
+__device__ __forceinline__ uint32_t dword_of(const uint4& v, int j) {
+  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
 // The float value of the low 16-bit value of v.
 template <int DT>
 __device__ __forceinline__ float mx_lo(uint32_t v) {

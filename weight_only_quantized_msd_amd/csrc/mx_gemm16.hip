@@ -17,10 +17,6 @@ namespace wqbmm {
 
 namespace {
 
-__device__ __forceinline__ uint32_t dword_of(const uint4& v, int j) {
-  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
-}
-
 template <int CT>
 __device__ __forceinline__ void mfma16_into(mx_f4& c, uint4 a, uint4 b) {
   const mx_i4 av = __builtin_bit_cast(mx_i4, a), bv = __builtin_bit_cast(mx_i4, b);

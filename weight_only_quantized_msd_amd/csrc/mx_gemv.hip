@@ -29,19 +29,13 @@ namespace {
 constexpr int GEMV_WAVES = 8;
 
 enum class Mode { kDirect, kSplit, kMxfp4 };
-
-__device__ __forceinline__ uint32_t dword_of(const uint4& v, int j) {
-  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
-}
 }  // namespace
 
 template <int DT>
 __device__ __forceinline__ void mx_store4(uint16_t* __restrict__ y, int64_t m, int64_t n, int64_t N, mx_f4 v) {
   uint16_t* p = y + m * N + n;
   if ((N & 3) == 0) {                       // then n + 3 < N, and the store is aligned
-    const uint32_t lo = mx_round16<DT>(v[0]) | ((uint32_t)mx_round16<DT>(v[1]) << 16);
-    const uint32_t hi = mx_round16<DT>(v[2]) | ((uint32_t)mx_round16<DT>(v[3]) << 16);
-    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    *reinterpret_cast<uint2*>(p) = mx_pack4<DT>(v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
