@@ -31,7 +31,7 @@ def calls(L):
 def child():
     sys.path.insert(0, os.path.dirname(HERE))
     from weight_only_quantized_msd_amd import _lib as L
-    stub = ctypes.CDLL(os.environ["LD_PRELOAD"])
+    stub = ctypes.CDLL(os.environ["HIP_STUB"])
     stub.stub_stream_of.restype = ctypes.c_size_t
     all_calls = calls(L)
 
@@ -89,8 +89,9 @@ def test_calls_of_several_threads(tmp_path):
     r = subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-isystem", include,
                         os.path.join(HERE, "hip_stub.cpp"), "-o", stub, "-lpthread"], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    r = subprocess.run([sys.executable, os.path.abspath(__file__)], env=dict(os.environ, LD_PRELOAD=stub),
-                       capture_output=True, text=True, timeout=100)
+    first = ":".join(filter(None, [stub, os.environ.get("LD_PRELOAD")]))
+    r = subprocess.run([sys.executable, os.path.abspath(__file__)],
+                       env=dict(os.environ, LD_PRELOAD=first, HIP_STUB=stub), capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and "threads ok" in r.stdout, r.stdout + r.stderr
 
 

@@ -2,6 +2,7 @@
 mx_api.cpp) under AddressSanitizer and UndefinedBehaviorSanitizer, as
 test_sanitized.py does for the int4 operator: their extents go up to 2^63 - 1."""
 import glob
+import os
 
 import pytest
 
@@ -14,5 +15,6 @@ def test_mxfp4_validation_under_asan_ubsan():
         pytest.skip("clang's ASan runtime is not installed")
     from weight_only_quantized_msd_amd.build import build_host_sanitized
     lib = build_host_sanitized()
-    out = _run({"LD_PRELOAD": rts[0], "WQBMM_LIB": lib}, ["tests/test_mxfp4.py", "-k", "c_abi or tiled_weight_bytes"])
+    first = ":".join(filter(None, [rts[0], os.environ.get("LD_PRELOAD")]))
+    out = _run({"LD_PRELOAD": first, "WQBMM_LIB": lib}, ["tests/test_mxfp4.py", "-k", "c_abi or tiled_weight_bytes"])
     assert "failed" not in out and "skipped" not in out
