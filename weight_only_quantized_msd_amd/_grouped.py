@@ -23,9 +23,12 @@ from ._lib import check, lib
 
 
 def _matrix(t, name):
-    """Checks a 2-D device tensor with contiguous rows, any distance apart; (rows, columns, row distance)."""
+    """Checks a 2-D device tensor with contiguous rows, any distance of at least their length apart; (rows,
+    columns, row distance)."""
     rows, cols, ld = _m._rows(t, name)
-    return rows, cols, max(ld, cols)
+    if ld < cols:            # expanded, or overlapping windows: the kernels count on rows of their own
+        raise ValueError(f"the rows of {name} must not overlap")
+    return rows, cols, ld
 
 
 def _index(t, dims, name, device):
