@@ -22,11 +22,11 @@ def calls(torch, W, wrap, **o):
         ("z", (S, H), half, lambda t: W.wqbmm_moe_combine(t, slots, weights)),
         ("base", (T, H), half, lambda t: W.wqbmm_moe_combine(z, slots, weights, base=t)),
         ("y", (T, H), half, lambda t: W.wqbmm_moe_combine(z, slots, weights, y=t)),
-        ("y", (T, H), half, lambda t: W.wqbmm_moe_combine(z, slots, weights, base=t, y=t)),
+        ("base", (T, H), half, lambda t: W.wqbmm_moe_combine(z, slots, weights, base=t, y=t)),
         ("x", (T, H), half, lambda t: W.wqbmm_lora_matmul(t, a, b, offsets, rows)),
         ("base", (T, H), half, lambda t: W.wqbmm_lora_matmul(x, a, b, offsets, rows, base=t)),
         ("y", (T, H), half, lambda t: W.wqbmm_lora_matmul(x, a, b, offsets, rows, base=base, y=t)),
-        ("y", (T, H), half, lambda t: W.wqbmm_lora_matmul(x, a, b, offsets, rows, base=t, y=t)),
+        ("base", (T, H), half, lambda t: W.wqbmm_lora_matmul(x, a, b, offsets, rows, base=t, y=t)),
     ]
 
 
