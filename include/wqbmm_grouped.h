@@ -19,9 +19,9 @@
  * launch, all work asynchronous on `stream`, workspace per (device, stream) with
  * the same growth and capture rules, deterministic results, gfx950 only.  Further
  * rules here:
- *   - Groups G: 1 to 1024.  Places S and rows: at most 2^24.  No rows (T, S or M
- *     of 0) is a no-op (but for group_rows, whose offsets become 0), and arrays with
- *     that extent may then be NULL.
+ *   - Groups G: 1 to 1024.  Places S and rows: at most 2^24.  S * N, T * H and M * N:
+ *     at most 2^38.  No rows (T, S or M of 0) is a no-op (but for group_rows, whose
+ *     offsets become 0), and arrays with that extent may then be NULL.
  *   - ld* is the distance between rows in elements: at least the row length and
  *     at most 2^36.  Matrices of 16-bit values are 16-byte aligned and their ld a
  *     multiple of 8 where nothing else is said; logits, index arrays and fp32

@@ -16,7 +16,7 @@ using namespace wqbmm;
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxK = int64_t(1) << 20;
 constexpr int64_t kMaxLd = int64_t(1) << 36;       // byte offsets stay within 64 bits
-constexpr int64_t kMaxResult = int64_t(1) << 38;   // values of a result: workgroups are counted in 31 bits
+constexpr int64_t kMaxResult = int64_t(1) << 38;   // values of a result: tiles are counted in 31 bits
 
 bool aligned(const void* p, int to = 16) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1)) == 0; }
 bool good_k(int64_t K) { return K > 0 && K <= kMaxK && K % kMxBlock == 0; }

@@ -13,6 +13,17 @@ constexpr int kLoraMaxR = 256;
 // A plan's tiles of `most` places, at most.
 inline int64_t group_tiles(int64_t S, int64_t G, int64_t most) { return S / most + (G < S ? G : S); }
 
+// A grid holds fewer than 2^32 threads: workgroups of 256 go in as many launches as that
+// takes, each told its first one's number.
+template <typename Go>
+hipError_t in_launches(int64_t workgroups, Go&& go) {
+  constexpr int64_t kMost = int64_t(1) << 23;
+  hipError_t e = hipSuccess;
+  for (int64_t first = 0; first < workgroups && e == hipSuccess; first += kMost)
+    e = go(first, dim3((unsigned)(workgroups - first < kMost ? workgroups - first : kMost)));
+  return e;
+}
+
 hipError_t launch_route(const void* logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, bool renormalize,
                         int32_t* ids, float* weights, hipStream_t stream);
 

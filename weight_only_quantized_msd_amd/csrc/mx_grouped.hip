@@ -65,15 +65,15 @@ __device__ __forceinline__ void few_rows(const Grouped& a, const GroupTile& t, i
 }
 
 template <int DT, bool ACT4, bool GATED, int P>
-__global__ __launch_bounds__(FEW_WAVES * 64) void mx_grouped_few_kernel(Grouped a, int pblocks) {
+__global__ __launch_bounds__(FEW_WAVES * 64) void mx_grouped_few_kernel(Grouped a, int pblocks, int first) {
   constexpr int MINE = 2 * PART_BYTES;
   static_assert(MINE >= P * 2 * 1024, "a wave's sums");
   __shared__ __attribute__((aligned(16))) uint8_t lds[FEW_WAVES * MINE];
   __shared__ int lists[FEW_WAVES][32];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pb = blockIdx.x % pblocks;
-  const GroupTile t = group_tile(a.offsets, a.G, a.S, 32, blockIdx.x / pblocks, false);
+  const int item = first + blockIdx.x, pb = item % pblocks;
+  const GroupTile t = group_tile(a.offsets, a.G, a.S, 32, item / pblocks, false);
   if (t.group < 0) return;                      // all waves find the same
   // The places' rows, each wave a list of its own; one outside x is read as row 0 and not used.
   int* const list = lists[wave];
@@ -99,7 +99,10 @@ static hipError_t few_dt(const Grouped& a, hipStream_t stream) {
   const int64_t tiles = group_tiles(a.S, a.G, 32);
   auto go = [&](auto* kernel, int panels) {
     const int pblocks = (a.n_out / kMxPanel + panels - 1) / panels;
-    return mx_launch(kernel, dim3((unsigned)(pblocks * tiles)), dim3(FEW_WAVES * 64), stream, a, pblocks);
+    return in_launches(pblocks * tiles, [&](int64_t from, dim3 grid) {      // up to 2^27: S * N <= 2^38
+      const int first = (int)from;
+      return mx_launch(kernel, grid, dim3(FEW_WAVES * 64), stream, a, pblocks, first);
+    });
   };
   const int four = GATED ? 2 : 4;               // panels of results of four panels of weights
   if ((a.n_out / kMxPanel + four - 1) / four * tiles <= 512) return go(mx_grouped_few_kernel<DT, ACT4, GATED, 2>, four / 2);
