@@ -115,10 +115,14 @@ __device__ __forceinline__ void lora_operands(mx_f4 (&v)[2], int units, uint4 (&
     for (int d = units / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     e = top == 0.0f ? 0 : 14 - __builtin_amdgcn_frexp_expf(top);     // below 2^14
     uint32_t h[4], l[4];
+    // part 0 is 0 for 0 alone: it rounds f and 2^-24 of its sign, which part 1 takes off again (B's infinities)
+    auto first = [](float f) __attribute__((always_inline)) {
+      return mx_round16<MX_F16>(f + fmaxf(fminf(f * 0x1p127f, 0x1p-24f), -0x1p-24f));
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float a = __builtin_ldexpf(v[i / 2][i % 2 * 2], e), b = __builtin_ldexpf(v[i / 2][i % 2 * 2 + 1], e);
-      h[i] = mx_round16<MX_F16>(a) | (uint32_t)mx_round16<MX_F16>(b) << 16;
+      h[i] = first(a) | (uint32_t)first(b) << 16;
       const float ra = a - mx_lo<MX_F16>(h[i]), rb = b - mx_hi<MX_F16>(h[i]);
       l[i] = mx_round16<MX_F16>(__builtin_isfinite(a) ? ra : 0.0f) |
              (uint32_t)mx_round16<MX_F16>(__builtin_isfinite(b) ? rb : 0.0f) << 16;
@@ -126,6 +130,25 @@ __device__ __forceinline__ void lora_operands(mx_f4 (&v)[2], int units, uint4 (&
     part[0] = make_uint4(h[0], h[1], h[2], h[3]);
     part[1] = make_uint4(l[0], l[1], l[2], l[3]);
   }
+}
+
+// B for v's later parts where it holds infinities: the largest finite values instead.  Part 0
+// makes the result infinite; a later one may be 0 or of the other sign, and 0 * inf or
+// inf - inf is NaN.  That only happens to results that come out NaN without this, so that the
+// products are made again where one does (this in every product: 37 -> 46 us for 2048 rows, rank
+// 128, 4096 x 4096, fp16).  Positive values order as 16-bit integers do, negative ones as
+// unsigned ones.
+template <int DT>
+__device__ __forceinline__ uint4 lora_finite(uint4 b) {
+  constexpr int16_t MOST = DT == MX_BF16 ? 0x7f7f : 0x7bff;
+  typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+  auto two = [](uint32_t w) __attribute__((always_inline)) {
+    const mx_u16x2 negative = {(uint16_t)(MOST | 0x8000), (uint16_t)(MOST | 0x8000)};
+    const i16x2 positive = {MOST, MOST};
+    const mx_u16x2 v = __builtin_elementwise_min(__builtin_bit_cast(mx_u16x2, w), negative);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(i16x2, v), positive));
+  };
+  return make_uint4(two(b.x), two(b.y), two(b.z), two(b.w));
 }
 
 template <int DT, int RC, int MT>
@@ -225,6 +248,26 @@ __global__ __launch_bounds__(LORA_WAVES * 64) void lora_up_kernel(Lora p, int sp
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      bool nan = false;
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        nan |= __builtin_isunordered(acc[c][m][0], acc[c][m][1]) || __builtin_isunordered(acc[c][m][2], acc[c][m][3]);
+      if (__any(nan)) {                           // the same bits again, but where B is infinite
+        int column = i16;
+        asm volatile("" : "+v"(column));          // no address is kept for this
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          const uint16_t* const br = p.b + ((int64_t)t.group * p.N + min(n0 + c * 16 + column, p.N - 1)) * p.r;
+          acc[c][m] = mx_f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int j = g * 8; j < RC * 32; j += 32) {
+            const uint4 bv = load8(br, j, p.r), rest = lora_finite<DT>(bv);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i)
+              acc[c][m] = mx_mfma16<DT>(i == 0 ? bv : rest, *reinterpret_cast<const uint4*>(&vs[i][m * 16 + i16][j]), acc[c][m]);
+          }
+        }
+      }
 #pragma unroll
       for (int c = 0; c < NT; ++c) *reinterpret_cast<mx_f4*>(mine + i16 * OUT + c * 16 + g * 4) = acc[c][m];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
