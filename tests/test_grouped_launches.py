@@ -1,5 +1,9 @@
 """The launches of the operators whose weights depend on the row, without a GPU."""
+import re
+
+import grouped_cases as C
 import kernel_launches as K
+import test_gpu_grouped as V
 
 # the ends of the sizes that include/wqbmm_grouped.h allows
 LARGEST = (
@@ -32,3 +36,42 @@ def test_the_largest_sizes_fit_their_launches(tmp_path):
             assert sum(g for _, g, _ in launches) >= tiles * -(-columns // wide), args
             few.add(len(launches) > 1)
     assert few == {False, True}
+
+
+def tiled_calls():
+    for name, (_, act, sizes, none, k, N, R) in C.TILED.items():
+        S = sum(sizes) + none
+        for dtype, code in C.TYPES.items():
+            for gated in (False, True):
+                yield name, dtype, gated, K.grouped(S, len(sizes), k, N, code, int(act == "mxfp4"), int(gated), R or S)
+
+
+def test_the_cases_reach_their_kernels(tmp_path):
+    cases = list(tiled_calls())
+    _, each = K.launched(tmp_path, [c[-1] for c in cases])
+    for (name, dtype, gated, _), (status, launches) in zip(cases, each):
+        assert status == 0 and launches[-1][0] == C.kernel(name, dtype, gated), (name, launches)
+
+
+def calls_of_the_tests():
+    """What the GPU tests of the values call, by its sizes."""
+    for T, E, k in V.ROUTES:
+        yield from (K.route(T, E, k, dtype) for dtype in (0, 1, 2))
+    marks = {m.args[0]: m.args[1] for m in V.test_group_rows.pytestmark if m.name == "parametrize"}
+    yield from (K.group(*sizes) for sizes in marks["T,k,groups"] + C.ROWS)
+    for T, k, groups, Kx, N, _ in V.GROUPED:
+        yield from (K.grouped(T * k, groups, Kx, N, dtype, act, gated, T)
+                    for dtype in (0, 1) for act in (0, 1) for gated in (0, 1))
+    for _, _, _, call in tiled_calls():
+        yield call
+    for M, L, r, Kx, N, _ in V.LORAS + C.LORAS:
+        yield from (K.lora(M, L, r, Kx, N, dtype) for dtype in (0, 1))
+    yield from (K.combine(96, 8, 2048, dtype) for dtype in (0, 1))
+
+
+def test_every_kernel_is_reached_by_a_test(tmp_path):
+    """Each instantiation that the library holds, by the cases of the tests that compare values on the GPU."""
+    kernels, each = K.launched(tmp_path, list(calls_of_the_tests()))
+    mine = {k for k in kernels if re.match(r"(route|group_rows|combine|lora_\w+|mx_grouped\w+|mx_row_codes)_kernel", k)}
+    assert len(mine) > 60
+    assert mine - {k for status, launches in each for k, _, _ in launches} == set()
