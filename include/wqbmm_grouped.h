@@ -31,7 +31,9 @@
  *     nowhere and written nowhere (each call says what becomes of it), and offsets
  *     that descend or lie outside [0, S] make y's values unspecified, no more.
  *   - Infinities and NaN are followed where they are chosen; what is left out
- *     (masked logits, choices of no group, rows of no group) has no effect.
+ *     (masked logits, choices of no group, rows of no group) has no effect.  MXFP4
+ *     weights of 2^128 and more are beyond the products with 16-bit x (wqbmm_mxfp4.h).
+ *   - An output overlaps no input, but for a y that is base.
  */
 #ifndef WQBMM_GROUPED_H
 #define WQBMM_GROUPED_H
@@ -97,9 +99,11 @@ wqbmm_status wqbmm_moe_combine(const void* z, int dtype, int64_t ldz, int64_t S,
                                int64_t ldy, void* stream);
 
 /*
- * y[m] = base[m] + scales[l] * B_l . (A_l . x[m]) for each row m of adapter l; rows
- * of none: y[m] = base[m].  Sums and A_l . x in fp32 (B multiplies them in at
- * least 22 bits), rounded once.  scales NULL: 1; base NULL: 0.
+ * y[m] = base[m] + B_l . (scales[l] * (A_l . x[m])) for each row m of adapter l; rows
+ * of none: y[m] = base[m].  Sums and scales[l] * (A_l . x) in fp32, y rounded once.  B
+ * multiplies the latter's values with 24 bits (BF16; those below 2^-110 to within
+ * 2^-133) or 22 (F16; those more than 2^16 below their row's largest to within 2^-38
+ * of it).  scales NULL: 1; base NULL: 0.
  *   x        [M][K], F16 or BF16 (rows ldx apart)
  *   a        [L][r][K], b [L][N][r], x's type, contiguous; r a multiple of 8, at
  *            most 256 (smaller adapters are padded with zeros); L <= 1024

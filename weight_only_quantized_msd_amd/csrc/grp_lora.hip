@@ -5,13 +5,16 @@
 // the waves of a workgroup, and over workgroups where there are few tiles of
 // rows), fp32 partial sums in the workspace; then B . v, a tile of rows and
 // columns a workgroup, added to base in registers.  v keeps fp32's sums; for the
-// 16-bit products with B it is taken apart: bf16, three parts of eight bits
-// (exact); fp16, two parts of eleven after a row's values are scaled by a power
-// of two to below 2^14 (22 bits; bf16 parts would need B taken apart as well).
+// 16-bit products with B it is taken apart: bf16, three parts of eight bits (exact down
+// to 2^-110); fp16, two parts of eleven after a row's values are scaled by a power of two
+// to below 2^14.  These hold 22 bits of a value, or 2^-38 of its row's largest where that is
+// more: part 1 ends at fp16's 2^-24, half of which is 2^-38 of the largest, 2^13 at least.
+// (bf16 parts would need B taken apart as well; a third fp16 part would take half as much
+// LDS again for v and leave two workgroups a CU at ranks 72 to 128, not three.)
 //
-// 48 rows, 16 adapters, rank 16, 4096 x 4096: 3.4 and 4.6 us, two launches of three trips to
-// memory each.  2048 rows, 5 adapters, rank 64, 4096 -> 11008: 11 us (x and A, 26 MB) and 27
-// (base and y, 90 MB, 3.4 TB/s, beside 120 MB of v and B from L2).
+// 48 rows, 16 adapters, rank 16, 4096 x 4096: 3.8 and 4.9 us, two launches of three trips to
+// memory each.  2048 rows, 5 adapters, rank 64, 4096 -> 11008: 11 us (x and A, 26 MB) and 28
+// (base and y, 90 MB, 3.2 TB/s, beside 120 MB of v and B from L2).
 #include <algorithm>
 
 #include "grp_device.hpp"
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(LORA_WAVES * 64) void lora_down_kernel(Lora p, int 
 // lane with four columns of a row, 32 bytes of it a store; by way of LDS of the wave's
 // own it loads base, ahead of the products, and stores y in 16 bytes a lane, 128 of a
 // row (2048 rows, rank 64, 11008 columns: 48 us without, 29 with).  The stores go past
-// the caches, which base and B need (29 -> 26 us, 3.5 TB/s).
+// the caches, which base and B need (29 -> 26 us; 28 with what B's infinities take).
 template <int DT>
 __device__ __forceinline__ void lora_operands(mx_f4 (&v)[2], int units, uint4 (&part)[3], int& e) {
   if constexpr (DT == MX_BF16) {
