@@ -3,9 +3,9 @@
 // one group, which it finds from the offsets, so that one launch serves any
 // distribution of the rows.  The waves share K (mx_expert.hpp).
 //
-// Bound by the weights' bytes after three trips to memory (offsets, rows, operands): 96 x
-// 2048 x 2048 gated (T, K, N), 64 experts, 8 chosen, 31 us (142 MB, 4.5 TB/s); one token
-// 5.1 us.
+// Bound by the weights' bytes after three trips to memory (offsets, rows, operands): 48 x
+// 2048 x 2048 gated (T, K, N), 64 experts, 8 chosen, weights from memory, 37 us (142 MB, 3.9
+// TB/s); one token 7.4 us, 5.6 with weights from the memory-side cache.
 #include "grp_device.hpp"
 #include "grp_launch.hpp"
 #include "mx_expert.hpp"
@@ -89,11 +89,12 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void mx_grouped_few_kernel(Grouped 
 }
 
 // Four panels a workgroup share the loads of its rows; two where the workgroups would make
-// two rounds of the CUs or fewer.  us, four and two: 1 x 2048 x 2048 gated (T, K, N), 64
-// experts, 8 chosen 5.6 and 5.1; 33 x 1056 x 1472 gated, 12, 3: 7.2 and 6.7; 16 x 11008 x
-// 4096, 8, 2: 30.5 and 31.6; 200 x 1024 x 2048 gated, 16, 2: 10.0 and 11.8; 96 x 2048 x
-// 2048 gated, 64, 8: 31.3 and 39.1.  (Rows loaded in place, not staged: 34.8 there; eight
-// panels: 37.0.  Tiles of 32 rows with 16 or fewer worked as 32: 33.8, and one token 7.0.)
+// two rounds of the CUs or fewer.  us, four and two, weights from memory: 1 x 2048 x 2048
+// gated (T, K, N), 64 experts, 8 chosen 8.1 and 7.4; 33 x 1056 x 1472 gated, 12, 3: 8.4 and
+// 8.9 (from the memory-side cache 7.2 and 6.7); 16 x 11008 x 4096, 8, 2: 40.2 and 41.0; 200 x
+// 1024 x 2048 gated, 16, 2: 12.2 and 14.8; 48 x 2048 x 2048 gated, 64, 8: 37.2 and 44.3.  (With
+// 96 tokens, which are the tiled kernels' now, from that cache, 31.3 and 39.1: rows loaded in
+// place, not staged, 34.8; eight panels 37.0; tiles of 16 or fewer rows worked as 32 33.8.)
 template <int DT, bool ACT4, bool GATED>
 static hipError_t few_dt(const Grouped& a, hipStream_t stream) {
   const int64_t tiles = group_tiles(a.S, a.G, 32);

@@ -4,10 +4,10 @@
 // that a wave has both of a result in its own accumulators); x's rows are copied
 // from where the plan says.
 //
-// 2047 x 2048 x 2048 gated (T, K, N), 64 experts of uneven size, 8 chosen, fp16: 129 us, 1.07
+// 2047 x 2048 x 2048 gated (T, K, N), 64 experts of uneven size, 8 chosen, fp16: 136 us, 1.01
 // PFLOP/s on the rows there are, bound by the conversion of W's codes beside the
-// products (64 rows of x share one) and by the rows that tiles leave empty.  96 tokens: 25
-// us, the weights' bytes at 5.7 TB/s.
+// products (64 rows of x share one) and by the rows that tiles leave empty.  96 tokens: 32
+// us a call among others on other weights, whose 142 MB come at 4.5 TB/s.
 #include "mx_gemm16.hpp"
 #include "mx_grouped_tile.hpp"
 
@@ -119,8 +119,9 @@ hipError_t launch_mx_grouped16(const Grouped& a, int dtype, bool gated, hipStrea
 
 // Tiles of 64 rows where there are about enough to fill the chip, from eight rows a group
 // on; else, and where x or an expert's weights pass 31 bits, the kernel of few rows, whose
-// workgroups are smaller and load less for a row that is not there.  us,
-// few rows and tiles (with how many there are, as counted here):
+// workgroups are smaller and load less for a row that is not there.  us on one set of inputs,
+// which the memory-side cache holds, few rows and tiles (with how many there are, as counted
+// here; from memory, 96 x 2048 x 2048 takes 41 and 35 with 16-bit x, 40 and 37 with MXFP4 x):
 //   16-bit x: 96 x 2048 x 2048 gated (T, K, N), 64 experts, 8 chosen (352) 30.4, 26.0;
 //   100 x 4096 x 22016 gated, 8, 2 (602) 103, 84; 700 x 1056 x 1472 gated, 12, 3 (228)
 //   27.9, 14.9; 300 x 4096 x 4096, 4, 1 (96) 25.1, 28.4; 200 x 1024 x 2048 gated, 16, 2 (112)
