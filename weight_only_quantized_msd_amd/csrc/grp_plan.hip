@@ -336,8 +336,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
                                                       const int32_t* __restrict__ slots,
                                                       const float* __restrict__ weights, int k, const uint16_t* base,
                                                       int64_t ldb, uint16_t* y, int64_t ldy, uint32_t units,
-                                                      int64_t count, int64_t first) {
-  const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;           // of count = T * units
+                                                      int64_t count, uint32_t first) {
+  const int64_t i = (int64_t)(first + blockIdx.x) * 256 + threadIdx.x;  // of count = T * units
   if (i >= count) return;
   const int64_t t = i / units, c = (i - t * units) * 8;
   float v[8] = {};
@@ -377,7 +377,8 @@ hipError_t launch_combine(const void* z, int dtype, int64_t ldz, int64_t S, int6
   const int64_t count = T * units;
   const int s = (int)S, kk = (int)k;
   auto* kernel = dtype == MX_F16 ? combine_kernel<MX_F16> : combine_kernel<MX_BF16>;
-  return in_launches((count + 255) / 256, [&](int64_t first, dim3 grid) {
+  return in_launches((count + 255) / 256, [&](int64_t from, dim3 grid) {    // up to 2^27: T * H <= 2^38
+    const uint32_t first = (uint32_t)from;
     return mx_launch(kernel, grid, dim3(256), stream, zp, ldz, s, slots, weights, kk, bp, ldb, yp, ldy, units, count,
                      first);
   });
